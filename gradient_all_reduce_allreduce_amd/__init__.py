@@ -18,7 +18,10 @@ from .api import (SUM, MEAN, F32, BF16, MAX_RANKS, DdpError, ddp_bucket_plan, dd
                   allreduce_multi_fused_sgd, allreduce_multi_ring_noalloc, ddp_set_wg_per_cu, KERNEL_FAMILIES,
                   allreduce_ring_buckets, allreduce_fused_sgd_buckets, zero1_sgd_step_buckets,
                   ddp_buckets_launch_count, reducescatter_ring_buckets, allgather_ring_buckets,
-                  allreduce_ring_stepwise_buckets, allreduce_hierarchical_buckets)
+                  allreduce_ring_stepwise_buckets, allreduce_hierarchical_buckets,
+                  NORM_WORKSPACE_BYTES, grad_norm_multi, grad_clip_multi, allreduce_ring_norm,
+                  allreduce_ring_norm_buckets, allreduce_norm_workspace_bytes, adamw_step_multi,
+                  MultiGrad, grad_norm, clip_grads, adamw_step, allreduce_norm)
 from .bucketer import GradBucketer
 
 __all__ = [
@@ -35,4 +38,7 @@ __all__ = [
     "allreduce_ring_buckets", "allreduce_fused_sgd_buckets", "zero1_sgd_step_buckets",
     "ddp_buckets_launch_count", "reducescatter_ring_buckets", "allgather_ring_buckets",
     "allreduce_ring_stepwise_buckets", "allreduce_hierarchical_buckets",
+    "NORM_WORKSPACE_BYTES", "grad_norm_multi", "grad_clip_multi", "allreduce_ring_norm",
+    "allreduce_ring_norm_buckets", "allreduce_norm_workspace_bytes", "adamw_step_multi",
+    "MultiGrad", "grad_norm", "clip_grads", "adamw_step", "allreduce_norm",
 ]

@@ -12,15 +12,21 @@ Python ints, stream as an int handle or None):
     allgather_ring_emulated, allgather_ring_buckets, allreduce_ring_stepwise,
     allreduce_ring_stepwise_buckets, allreduce_tree_emulated, allreduce_hierarchical_buckets,
     allreduce_hierarchical_emulated, ddp_multi_plan, ddp_multi_block_map, allreduce_multi_ring_emulated,
-    allreduce_multi_fused_sgd, allreduce_multi_ring_noalloc, ddp_set_wg_per_cu
+    allreduce_multi_fused_sgd, allreduce_multi_ring_noalloc, grad_norm_multi, grad_clip_multi,
+    allreduce_ring_norm, allreduce_ring_norm_buckets, allreduce_norm_workspace_bytes,
+    adamw_step_multi, ddp_set_wg_per_cu
 Tensor-level helpers:
     allreduce(tensors, op, chunking, out)            -> list of outputs
     allreduce_sgd(grads, w, v, lr, mu, op, chunking, out)
     zero1_sgd_step(grads, w, v, lr, mu, params, op, chunking)
     reduce_scatter, all_gather, allreduce_stepwise, allreduce_tree,
     allreduce_hierarchical, MultiAllReduce
+    allreduce_norm(tensors, op, chunking, out)       -> (outputs, norm)
+    grad_norm(grads), clip_grads(grads, max_norm), adamw_step(grads, w, m, v, lr, step),
+    MultiGrad(grads)
 """
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -32,6 +38,7 @@ MEAN = N.DDP_MEAN
 F32 = N.DDP_F32
 BF16 = N.DDP_BF16
 MAX_RANKS = N.DDP_MAX_RANKS
+NORM_WORKSPACE_BYTES = N.DDP_NORM_WORKSPACE_BYTES
 
 
 class DdpError(RuntimeError):
@@ -303,6 +310,73 @@ def allreduce_multi_ring_noalloc(op, P, chunking, numels, in_ptrs, in_dtype, out
     _check(N.lib().allreduce_multi_ring_noalloc(
         _op(op), P, chunking, T, numels.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)),
         N.pointer_array(in_ptrs), in_dtype, N.pointer_array(out_ptrs), out_dtype, stream))
+
+
+def _long_array(values):
+    return (ctypes.c_int64 * len(values))(*values)
+
+
+def _int_array(values):
+    return (ctypes.c_int32 * len(values))(*values)
+
+
+def grad_norm_multi(numels, ptrs, dtypes, workspace, workspace_bytes, norm, stream=None):
+    """The global 2-norm of tensors given by host lists: T element counts,
+    device addresses and dtype codes.  ``workspace`` (device, at least
+    NORM_WORKSPACE_BYTES) and ``norm`` (one float) are device addresses."""
+    if not len(numels) == len(ptrs) == len(dtypes):
+        raise ValueError("numels, ptrs and dtypes must have one entry per tensor")
+    _check(N.lib().grad_norm_multi(len(numels), _long_array(numels), N.pointer_array(ptrs), _int_array(dtypes),
+                                   workspace, workspace_bytes, norm, stream))
+
+
+def grad_clip_multi(numels, ptrs, dtypes, out, max_norm, norm_given, norm, workspace, workspace_bytes,
+                    stream=None):
+    """Clipping of tensors given by host lists (``out``: T addresses)."""
+    if not len(numels) == len(ptrs) == len(dtypes) == len(out):
+        raise ValueError("numels, ptrs, dtypes and out must have one entry per tensor")
+    _check(N.lib().grad_clip_multi(len(numels), _long_array(numels), N.pointer_array(ptrs), _int_array(dtypes),
+                                   N.pointer_array(out), max_norm, int(bool(norm_given)), norm, workspace,
+                                   workspace_bytes, stream))
+
+
+def allreduce_ring_norm(op, P, chunking, rank_in, in_dtype, rank_out, out_dtype, n, norm, workspace,
+                        workspace_bytes, stream=None):
+    """``rank_out``: P addresses, or one (a single copy of the result)."""
+    _check(N.lib().allreduce_ring_norm(_op(op), P, chunking, N.pointer_array(rank_in), in_dtype, len(rank_out),
+                                       N.pointer_array(rank_out), out_dtype, n, norm, workspace,
+                                       workspace_bytes, stream))
+
+
+def allreduce_ring_norm_buckets(op, P, chunking, rank_in, in_dtype, rank_out, out_dtype, n, bucket_elems,
+                                norm, workspace, workspace_bytes, stream=None):
+    _check(N.lib().allreduce_ring_norm_buckets(_op(op), P, chunking, N.pointer_array(rank_in), in_dtype,
+                                               len(rank_out), N.pointer_array(rank_out), out_dtype, n,
+                                               bucket_elems, norm, workspace, workspace_bytes, stream))
+
+
+def allreduce_norm_workspace_bytes(P, chunking, in_dtype, out_dtype, n, bucket_elems=0):
+    """Workspace of the two calls above (host only); bucket_elems 0: one
+    bucket."""
+    b = ctypes.c_int64(0)
+    _check(N.lib().allreduce_norm_workspace_bytes(P, chunking, in_dtype, out_dtype, n, bucket_elems,
+                                                  ctypes.byref(b)))
+    return b.value
+
+
+def adamw_step_multi(numels, grads, grad_dtype, w, m, v, params, param_dtype, lr, beta1, beta2, eps,
+                     weight_decay, step, step_dev=None, norm=None, max_norm=0.0, stream=None):
+    """One AdamW step on tensors given by host lists of device addresses
+    (``params``: T addresses or None; ``step_dev``, ``norm``: device
+    addresses or None)."""
+    for x in (grads, w, m, v) + ((params,) if params is not None else ()):
+        if len(x) != len(numels):
+            raise ValueError("every list must have one entry per tensor")
+    _check(N.lib().adamw_step_multi(len(numels), _long_array(numels), N.pointer_array(grads), grad_dtype,
+                                    N.pointer_array(w), N.pointer_array(m), N.pointer_array(v),
+                                    N.pointer_array(params) if params is not None else None, param_dtype,
+                                    lr, beta1, beta2, eps, weight_decay, step, step_dev, norm, max_norm,
+                                    stream))
 
 
 def ddp_set_wg_per_cu(family, wg_per_cu):
@@ -715,3 +789,218 @@ def allreduce_sgd(grads, w, v, lr, mu, op="mean", chunking=None, out=None, bucke
                         torch_dtype_code(grads[0].dtype), grads[0].numel(), w.data_ptr(),
                         v.data_ptr(), lr, mu, out_ptrs, out_code, current_stream(grads[0].device))
     return out
+
+
+# ------------------------------------------- norm, clipping, AdamW --------
+
+@contextlib.contextmanager
+def _other_device(device):
+    import torch
+    with torch.cuda.device(device):
+        yield
+
+
+def _on(device):
+    """A context in which ``device`` is current: launches on its default
+    stream, which has no device of its own, go there too."""
+    import torch
+    if device.index is None or torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return _other_device(device)
+
+
+def _tensor_list(tensors, what, dtypes):
+    import torch
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    if not tensors:
+        raise ValueError(f"{what}: need at least one tensor")
+    device = tensors[0].device
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError(f"{what}: tensors must live on the GPU")
+        if t.device != device:
+            raise ValueError(f"{what}: every tensor must live on the same GPU")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what}: unsupported element type {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: tensors must be contiguous")
+    return tensors
+
+
+def _scalar(x, dtype, device, what):
+    """A one-element GPU tensor that a call reads."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.numel() != 1 or x.device != device:
+        raise ValueError(f"{what} must be a tensor of one {dtype} on the gradients' device")
+    return x
+
+
+class MultiGrad:
+    """Global norm, clipping and the AdamW step of one replica's gradients,
+    many tensors per launch.  ``grads``: GPU tensors (or one), contiguous,
+    float32 or bfloat16, mixed as they come.  They are checked and their
+    addresses taken once; every call works on those same tensors, which this
+    object keeps alive, and is enqueued on the stream current at the call.
+    Gradients that are replaced by new tensors (zero_grad(set_to_none=True))
+    need a new MultiGrad.  Calls may overlap on several streams and be captured
+    into graphs: each takes its own workspace from torch's allocator."""
+
+    def __init__(self, grads):
+        import torch
+        self.grads = _tensor_list(grads, "MultiGrad", (torch.float32, torch.bfloat16))
+        self.device = self.grads[0].device
+        self._numels = _long_array([g.numel() for g in self.grads])
+        self._ptrs = N.pointer_array([g.data_ptr() for g in self.grads])
+        self._dtypes = _int_array([torch_dtype_code(g.dtype) for g in self.grads])
+
+    def _match(self, tensors, what, dtypes):
+        """Tensors of the gradients' sizes, one each, on their device."""
+        tensors = _tensor_list(tensors, what, dtypes)
+        if len(tensors) != len(self.grads) or tensors[0].device != self.device or \
+                any(x.numel() != g.numel() for x, g in zip(tensors, self.grads)):
+            raise ValueError(f"{what}: need one tensor of each gradient's size on its device")
+        return tensors, N.pointer_array([x.data_ptr() for x in tensors])
+
+    def _workspace(self):
+        import torch
+        return torch.empty(NORM_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
+
+    def norm(self):
+        """The global 2-norm of all gradients, a float32 scalar tensor."""
+        import torch
+        with _on(self.device):
+            ws = self._workspace()
+            norm = torch.empty((), dtype=torch.float32, device=self.device)
+            _check(N.lib().grad_norm_multi(len(self.grads), self._numels, self._ptrs, self._dtypes, ws.data_ptr(),
+                                           NORM_WORKSPACE_BYTES, norm.data_ptr(), current_stream(self.device)))
+        return norm
+
+    def bind_clip(self, out=None):
+        """Returns ``run(max_norm, norm=None)``, which scales every gradient
+        by min(1, max_norm / (norm + 1e-6)), into ``out`` (one tensor per
+        gradient, of its type; default: in place), and returns the norm:
+        the gradients' own, computed in the same call, or the ``norm`` given
+        (a float32 scalar tensor, e.g. of ``allreduce_norm``)."""
+        import torch
+        if out is None:
+            out, optrs = self.grads, self._ptrs
+        else:
+            out, optrs = self._match(out, "clip out", (torch.float32, torch.bfloat16))
+            if any(o.dtype != g.dtype for o, g in zip(out, self.grads)):
+                raise ValueError("clip out: every output must have its gradient's type")
+
+        def run(max_norm, norm=None):
+            given = norm is not None
+            with _on(self.device):
+                ws = None
+                if given:
+                    _scalar(norm, torch.float32, self.device, "norm")
+                else:
+                    norm = torch.empty((), dtype=torch.float32, device=self.device)
+                    ws = self._workspace()
+                _check(N.lib().grad_clip_multi(len(self.grads), self._numels, self._ptrs, self._dtypes, optrs,
+                                               max_norm, given, norm.data_ptr(),
+                                               ws.data_ptr() if ws is not None else None,
+                                               NORM_WORKSPACE_BYTES if ws is not None else 0,
+                                               current_stream(self.device)))
+            return norm
+
+        run.tensors = (self.grads, out)
+        return run
+
+    def bind_adamw(self, w, m, v, params=None):
+        """Returns ``run(lr, step, betas=(0.9, 0.999), eps=1e-8,
+        weight_decay=0.01, norm=None, max_norm=None)``: one AdamW step on the
+        float32 master weights ``w`` and moments ``m`` and ``v`` (one tensor
+        per gradient, updated in place), writing the new weights also to
+        ``params`` (float32 or bfloat16) if given.  ``step``: the step's
+        number from 1, an int or a tensor of one int64 on the GPU (read when
+        the step runs, so that a captured step can be replayed).  With
+        ``norm`` (a float32 scalar tensor) and ``max_norm`` the gradient is
+        clipped on the way, and a norm that is not finite leaves the step
+        out.  The gradients must all have one type."""
+        import torch
+        if any(g.dtype != self.grads[0].dtype for g in self.grads):
+            raise ValueError("adamw: gradients must all have the same element type")
+        gcode = torch_dtype_code(self.grads[0].dtype)
+        w, wptrs = self._match(w, "adamw w", (torch.float32,))
+        m, mptrs = self._match(m, "adamw m", (torch.float32,))
+        v, vptrs = self._match(v, "adamw v", (torch.float32,))
+        pptrs, pcode = None, F32
+        if params is not None:
+            params, pptrs = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
+            if any(p.dtype != params[0].dtype for p in params):
+                raise ValueError("adamw: params must all have the same element type")
+            pcode = torch_dtype_code(params[0].dtype)
+
+        def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
+            if (norm is None) != (max_norm is None):
+                raise ValueError("adamw: norm and max_norm come together")
+            step_dev = None
+            if isinstance(step, torch.Tensor):
+                step_dev = _scalar(step, torch.int64, self.device, "step").data_ptr()
+                step = 0
+            if norm is not None:
+                norm = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
+            with _on(self.device):
+                _check(N.lib().adamw_step_multi(len(self.grads), self._numels, self._ptrs, gcode, wptrs, mptrs,
+                                                vptrs, pptrs, pcode, lr, betas[0], betas[1], eps, weight_decay,
+                                                step, step_dev, norm, max_norm if norm is not None else 0.0,
+                                                current_stream(self.device)))
+
+        run.tensors = (self.grads, w, m, v, params)
+        return run
+
+
+def grad_norm(grads):
+    """The global 2-norm of one replica's gradient tensors (float32 scalar
+    tensor); see ``MultiGrad``, which a loop over the same tensors keeps."""
+    return MultiGrad(grads).norm()
+
+
+def clip_grads(grads, max_norm, norm=None, out=None):
+    """Scale gradient tensors so that their global 2-norm is at most
+    ``max_norm``; returns the norm before.  See ``MultiGrad.bind_clip``."""
+    return MultiGrad(grads).bind_clip(out)(max_norm, norm)
+
+
+def adamw_step(grads, w, m, v, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params=None,
+               norm=None, max_norm=None):
+    """One AdamW step on lists of tensors (or one flat buffer each); see
+    ``MultiGrad.bind_adamw``."""
+    MultiGrad(grads).bind_adamw(w, m, v, params)(lr, step, betas, eps, weight_decay, norm, max_norm)
+
+
+def allreduce_norm(tensors, op="sum", chunking=None, out=None, out_dtype=None, bucket_elems=None):
+    """``allreduce`` that also leaves the global 2-norm of the result as one
+    rank holds it; returns (outputs, norm), the norm a float32 scalar tensor.
+    ``out``: P tensors, or a list of one: a single copy of the result (what
+    an optimizer step on one copy of the master weights reads).  Other
+    arguments as for ``allreduce``."""
+    import torch
+    tensors = _rank_tensors(tensors, "allreduce_norm")
+    P = len(tensors)
+    if out is None:
+        dt = out_dtype or tensors[0].dtype
+        out = [torch.empty(tensors[0].shape, dtype=dt, device=tensors[0].device) for _ in range(P)]
+    out = _rank_tensors(out, "allreduce_norm out")
+    if len(out) not in (1, P) or out[0].numel() != tensors[0].numel():
+        raise ValueError("allreduce_norm: out must match the inputs, P tensors or one")
+    _same_device(tensors, out, "allreduce_norm")
+    device = tensors[0].device
+    n = tensors[0].numel()
+    icode, ocode = torch_dtype_code(tensors[0].dtype), torch_dtype_code(out[0].dtype)
+    C = chunking or P
+    if bucket_elems is not None and bucket_elems < 1:
+        raise ValueError("allreduce_norm: bucket_elems must be at least 1")
+    need = allreduce_norm_workspace_bytes(P, C, icode, ocode, n, bucket_elems or 0)
+    with _on(device):
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        ins, outs = [t.data_ptr() for t in tensors], [t.data_ptr() for t in out]
+        end = (norm.data_ptr(), ws.data_ptr(), need, current_stream(device))
+        if bucket_elems is not None:
+            allreduce_ring_norm_buckets(op, P, C, ins, icode, outs, ocode, n, bucket_elems, *end)
+        else:
+            allreduce_ring_norm(op, P, C, ins, icode, outs, ocode, n, *end)
+    return out, norm

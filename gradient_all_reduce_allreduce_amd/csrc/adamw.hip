@@ -1,0 +1,272 @@
+// adamw.hip -- one AdamW step on many tensors, the gradient clipped on the
+// way, for gfx950.
+//
+// With c = min(1, max_norm / (norm + 1e-6)) (1 without a norm), t the step's
+// number from 1, and per element, float32 with one rounding per operation:
+//     g = c * g
+//     m = b1 * m + (1 - b1) * g
+//     v = b2 * v + (1 - b2) * (g * g)
+//     w = w * (1 - lr * wd) - lr / (1 - b1^t) * (m / (sqrt(v) / sqrt(1 - b2^t) + eps))
+// The factors that are the same for every element (1 - b1, 1 - lr * wd,
+// lr / (1 - b1^t), 1 / sqrt(1 - b2^t)) are computed in float64 and rounded to
+// float32 once: 1 - b2 taken in float32 would be off by 5e-5 for b2 = 0.999.
+// w, m and v are float32 and updated in place; a copy of the new weights
+// goes out as float32 or bf16 (nearest even).  A norm that is not finite
+// leaves everything as it was.
+//
+// Bound by HBM: gradient, w, m and v are read once and w, m, v and the copy
+// written once, 28 or 32 bytes an element, against some forty instructions
+// (a correctly rounded division and square root among them).
+//
+// Layout: tiles of kTileElems elements that start on the lines of w (the
+// first of a tensor whose w starts inside a line is short), every lane 4
+// consecutive elements of each stream; the other streams usually lie the
+// same way and are read as they lie if not.  Addresses and sizes travel in the
+// kernel arguments, several launches for more tensors than fit.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "grad_vec.h"
+#include "launch_grads.h"
+
+namespace ddp {
+namespace {
+
+using rr::u32x2;
+using rr::u32x4;
+
+constexpr int kBlock = 256;
+constexpr int kVecPerLane = 2;
+constexpr uint32_t kTileElems = kBlock * kVecPerLane * 4;
+constexpr uint32_t kLineElems = 32;                    // float32 per 128-byte line
+constexpr int64_t kMaxTiles = int64_t(1) << 30;
+constexpr int kCap = 144;                              // tensors per launch
+constexpr int kMaxGrid = 2048;
+
+struct AdamWArgs {
+    const char* g[kCap];
+    char* w[kCap];
+    char* m[kCap];
+    char* v[kCap];
+    char* p[kCap];
+    uint64_t numel[kCap];
+    uint32_t first_tile[kCap + 1];
+    int32_t n;
+    const float* norm;
+    const int64_t* step;     // device; null: step_size and root2 hold the step's
+    double b1, b2, lr;       // with `step`
+    float max_norm;
+    float beta1, beta2;
+    float one_beta1, one_beta2;
+    float decay;
+    float eps;
+    float step_size;
+    float root2;
+};
+static_assert(sizeof(AdamWArgs) <= 7800, "kernel arguments must stay under the 8,000 bytes measured to pass");
+typedef const __attribute__((address_space(4))) AdamWArgs* KAdamW;
+
+// b^t for t >= 1, float64, by squaring.
+__host__ __device__ __forceinline__ double power(double b, int64_t t) {
+    double r = 1.0;
+    for (; t > 0; t >>= 1) {
+        if (t & 1) r *= b;
+        b *= b;
+    }
+    return r;
+}
+
+struct Factors {
+    float c, beta1, beta2, one_beta1, one_beta2, decay, eps, step_size, root2;
+};
+
+__device__ __forceinline__ void adamw_element(float g, float& w, float& m, float& v, const Factors& f) {
+#pragma clang fp contract(off)
+    g = g * f.c;
+    const float m0 = f.beta1 * m;
+    const float m1 = f.one_beta1 * g;
+    m = m0 + m1;
+    const float v0 = f.beta2 * v;
+    const float gg = g * g;
+    const float v1 = f.one_beta2 * gg;
+    v = v0 + v1;
+    const float r = __builtin_sqrtf(v) * f.root2;
+    const float d = r + f.eps;
+    const float q = m / d;
+    const float w0 = w * f.decay;
+    const float s = f.step_size * q;
+    w = w0 - s;
+}
+
+template <bool GB, int PM>   // bf16 gradients; copy: 0 none, 1 float32, 2 bf16
+__global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs) {
+    const KAdamW a = (KAdamW)(__builtin_amdgcn_kernarg_segment_ptr());
+    constexpr uint32_t GES = GB ? 2 : 4;
+    constexpr uint32_t PES = PM == 2 ? 2 : 4;
+    Factors f;
+    f.c = 1.0f;
+    if (a->norm != nullptr) {
+        const float norm = *a->norm;
+        if (!(__builtin_fabsf(norm) < __builtin_inff())) return;
+        f.c = gv::clip_factor(norm, a->max_norm);
+    }
+    f.step_size = a->step_size;
+    f.root2 = a->root2;
+    if (a->step != nullptr) {
+        const int64_t t = *a->step;
+        if (t < 1) return;
+        f.step_size = static_cast<float>(a->lr / (1.0 - power(a->b1, t)));
+        f.root2 = static_cast<float>(1.0 / __builtin_sqrt(1.0 - power(a->b2, t)));
+    }
+    f.beta1 = a->beta1;
+    f.beta2 = a->beta2;
+    f.one_beta1 = a->one_beta1;
+    f.one_beta2 = a->one_beta2;
+    f.decay = a->decay;
+    f.eps = a->eps;
+
+    const uint64_t tiles = a->first_tile[a->n];
+    const uint32_t first = static_cast<uint32_t>(tiles * blockIdx.x / gridDim.x);
+    const uint32_t last = static_cast<uint32_t>(tiles * (blockIdx.x + 1) / gridDim.x);
+    int t = 0;
+    for (int h = a->n - 1; t < h;) {
+        const int mid = (t + h + 1) >> 1;
+        if (a->first_tile[mid] <= first) t = mid; else h = mid - 1;
+    }
+    for (uint32_t tile = first; tile < last; ++tile) {
+        while (tile >= a->first_tile[t + 1]) ++t;
+        const char* const g = a->g[t];
+        char* const w = a->w[t];
+        char* const m = a->m[t];
+        char* const v = a->v[t];
+        char* const p = a->p[t];
+        const int64_t n = static_cast<int64_t>(a->numel[t]);
+        const int64_t lead = static_cast<int64_t>((reinterpret_cast<uint64_t>(w) >> 2) % kLineElems);
+        const int64_t at = static_cast<int64_t>(tile - a->first_tile[t]) * kTileElems - lead;
+        if (at >= 0 && at + kTileElems <= n) {
+            u32x4 gq[kVecPerLane], wq[kVecPerLane], mq[kVecPerLane], vq[kVecPerLane];
+#pragma unroll
+            for (int u = 0; u < kVecPerLane; ++u) {
+                const int64_t i = at + (u * kBlock + threadIdx.x) * 4;
+                if constexpr (GB) {
+                    const u32x2 h = gv::load2_nt(g + i * 2);
+                    gq[u] = u32x4{h[0], h[1], 0u, 0u};
+                } else {
+                    gq[u] = gv::load4_nt(g + i * 4);
+                }
+                wq[u] = gv::load4_nt(w + i * 4);
+                mq[u] = gv::load4_nt(m + i * 4);
+                vq[u] = gv::load4_nt(v + i * 4);
+            }
+#pragma unroll
+            for (int u = 0; u < kVecPerLane; ++u) {
+                const int64_t i = at + (u * kBlock + threadIdx.x) * 4;
+                float wn[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float me = __uint_as_float(mq[u][e]);
+                    float ve = __uint_as_float(vq[u][e]);
+                    wn[e] = __uint_as_float(wq[u][e]);
+                    adamw_element(rr::elem<GB>(gq[u], e), wn[e], me, ve, f);
+                    wq[u][e] = __float_as_uint(wn[e]);
+                    mq[u][e] = __float_as_uint(me);
+                    vq[u][e] = __float_as_uint(ve);
+                }
+                gv::store4_nt(w + i * 4, wq[u]);
+                gv::store4_nt(m + i * 4, mq[u]);
+                gv::store4_nt(v + i * 4, vq[u]);
+                if constexpr (PM == 1) gv::store4_nt(p + i * 4, wq[u]);
+                if constexpr (PM == 2)
+                    gv::store2_nt(p + i * 2, u32x2{rr::bf16_bits(wn[0]) | (rr::bf16_bits(wn[1]) << 16),
+                                                   rr::bf16_bits(wn[2]) | (rr::bf16_bits(wn[3]) << 16)});
+            }
+            continue;
+        }
+        // A tensor's first or last tile: one element per lane.
+        const int64_t lo = at < 0 ? 0 : at;
+        const int64_t hi = at + kTileElems < n ? at + kTileElems : n;
+        for (int64_t i = lo + threadIdx.x; i < hi; i += kBlock) {
+            float* const we = reinterpret_cast<float*>(w) + i;
+            float* const me = reinterpret_cast<float*>(m) + i;
+            float* const ve = reinterpret_cast<float*>(v) + i;
+            float x = *we, y = *me, z = *ve;
+            adamw_element(gv::load_elem<GB>(g + i * GES), x, y, z, f);
+            *we = x;
+            *me = y;
+            *ve = z;
+            if constexpr (PM != 0) gv::store_elem<PM == 2>(p + i * PES, x);
+        }
+    }
+}
+
+const void* kernel_for(const AdamWLaunch& l) {
+    const int pm = l.params == nullptr ? 0 : (l.param_bf16 ? 2 : 1);
+    if (l.grad_bf16) {
+        return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<true, 0>)
+               : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<true, 1>)
+                         : reinterpret_cast<const void*>(&adamw_kernel<true, 2>);
+    }
+    return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<false, 0>)
+           : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<false, 1>)
+                     : reinterpret_cast<const void*>(&adamw_kernel<false, 2>);
+}
+
+}  // namespace
+
+int launch_adamw(const AdamWLaunch& l, const char** msg) {
+    AdamWArgs a;
+    a.norm = l.norm;
+    a.max_norm = l.max_norm;
+    a.step = l.step_dev;
+    a.b1 = l.beta1;
+    a.b2 = l.beta2;
+    a.lr = l.lr;
+    a.beta1 = static_cast<float>(l.beta1);
+    a.beta2 = static_cast<float>(l.beta2);
+    a.one_beta1 = static_cast<float>(1.0 - l.beta1);
+    a.one_beta2 = static_cast<float>(1.0 - l.beta2);
+    a.decay = static_cast<float>(1.0 - l.lr * l.weight_decay);
+    a.eps = static_cast<float>(l.eps);
+    a.step_size = 0.0f;
+    a.root2 = 0.0f;
+    if (l.step_dev == nullptr) {
+        a.step_size = static_cast<float>(l.lr / (1.0 - power(l.beta1, l.step)));
+        a.root2 = static_cast<float>(1.0 / std::sqrt(1.0 - power(l.beta2, l.step)));
+    }
+    const void* fn = kernel_for(l);
+    for (int32_t t = 0; t < l.n_tensors;) {
+        int64_t tiles = 0;
+        a.n = 0;
+        for (; t < l.n_tensors && a.n < kCap; ++t) {
+            const int64_t n = l.numels[t];
+            if (n == 0) continue;
+            const int64_t lead = static_cast<int64_t>((reinterpret_cast<uintptr_t>(l.w[t]) >> 2) % kLineElems);
+            const int64_t need = (lead + n + kTileElems - 1) / kTileElems;
+            if (tiles + need > kMaxTiles) break;
+            a.g[a.n] = static_cast<const char*>(l.grads[t]);
+            a.w[a.n] = reinterpret_cast<char*>(l.w[t]);
+            a.m[a.n] = reinterpret_cast<char*>(l.m[t]);
+            a.v[a.n] = reinterpret_cast<char*>(l.v[t]);
+            a.p[a.n] = l.params != nullptr ? static_cast<char*>(l.params[t]) : nullptr;
+            a.numel[a.n] = static_cast<uint64_t>(n);
+            a.first_tile[a.n] = static_cast<uint32_t>(tiles);
+            tiles += need;
+            ++a.n;
+        }
+        if (a.n == 0) continue;
+        a.first_tile[a.n] = static_cast<uint32_t>(tiles);
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, kMaxGrid));
+        void* args[] = {&a};
+        const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kBlock), args, 0, static_cast<hipStream_t>(l.stream));
+        if (e != hipSuccess) {
+            *msg = "hipLaunchKernel(adamw)";
+            return static_cast<int>(e);
+        }
+    }
+    return 0;
+}
+
+}  // namespace ddp

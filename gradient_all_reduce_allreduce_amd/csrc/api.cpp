@@ -15,12 +15,15 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <stdexcept>
 #include <string>
 #include <utility>
 #include <vector>
 
 #include "launch.h"
 #include "launch_copy.h"
+#include "launch_grads.h"
 #include "launch_multi.h"
 #include "launch_step.h"
 
@@ -110,9 +113,8 @@ int hip_fail(int code, const char* msg) {
     return fail(DDP_E_HIP, "HIP error %d in %s", code, msg ? msg : "?");
 }
 
-// Shared validation of the reduction calls.
-int validate_reduce(int op, int32_t P, int32_t chunking, const void* const* in, int in_dtype,
-                    void* const* out, int out_dtype, int64_t n, bool out_required) {
+// Shared validation of the reduction calls, but for their buffers.
+int validate_shape(int op, int32_t P, int32_t chunking, int in_dtype, int out_dtype, int64_t n) {
     if (op != DDP_SUM && op != DDP_MEAN) return fail(DDP_E_ARG, "unknown reduce op %d", op);
     int s = check_ranks(P);
     if (s) return s;
@@ -120,6 +122,14 @@ int validate_reduce(int op, int32_t P, int32_t chunking, const void* const* in, 
     if (int e = check_length(n, "n")) return e;
     if (!valid_dtype(in_dtype)) return fail(DDP_E_ARG, "unknown input dtype %d", in_dtype);
     if (!valid_dtype(out_dtype)) return fail(DDP_E_ARG, "unknown output dtype %d", out_dtype);
+    return DDP_OK;
+}
+
+// Shared validation of the reduction calls.
+int validate_reduce(int op, int32_t P, int32_t chunking, const void* const* in, int in_dtype,
+                    void* const* out, int out_dtype, int64_t n, bool out_required) {
+    int s = validate_shape(op, P, chunking, in_dtype, out_dtype, n);
+    if (s) return s;
     if ((s = check_ptr_array(in, P, "rank_in"))) return s;
     if (out_required || out != nullptr) {
         if ((s = check_ptr_array(const_cast<const void* const*>(out), P, "rank_out"))) return s;
@@ -191,6 +201,7 @@ std::vector<BucketPart> bucket_parts(const ddp::RingLaunch& l, int64_t E) {
 int launch_buckets(const ddp::RingLaunch& l, int64_t E, const char** msg) {
     const int ies = l.in_bf16 ? 2 : 4;
     const int oes = l.out_bf16 ? 2 : 4;
+    int64_t partials = 0;   // all-reduce with norm: workgroups so far
     for (const BucketPart& p : bucket_parts(l, E)) {
         ddp::RingLaunch b = l;
         for (int r = 0; r < l.P; ++r) {
@@ -203,6 +214,10 @@ int launch_buckets(const ddp::RingLaunch& l, int64_t E, const char** msg) {
         b.chunking = p.chunking;
         b.seg2 = p.seg2;
         b.seg2_chunking = p.seg2_chunking;
+        if (l.partials) {
+            b.partials = l.partials + partials;
+            partials += ddp::ring_workgroups(b);
+        }
         if (const int e = ddp::launch_ring_reduce(b, msg)) return e;
     }
     return 0;
@@ -1301,6 +1316,352 @@ int allreduce_multi_ring_noalloc(ddp_reduce_op op, int32_t P, int32_t chunking, 
     e = ddp::launch_multi_ring(l, &msg);
     if (e != 0) return hip_fail(e, msg);
     return ok();
+}
+
+}  // extern "C"
+
+// ---- gradient norm, clipping, AdamW -------------------------------------------
+
+namespace {
+
+static_assert(DDP_NORM_WORKSPACE_BYTES == ddp::kNormPartials * sizeof(double), "workspace size in the header");
+
+// A buffer of a many-tensor call: what it is, and whether the call writes it.
+struct Span {
+    uintptr_t lo;
+    uintptr_t hi;
+    bool written;
+    const char* what;
+    int32_t index;
+};
+
+// Nothing the call writes may overlap anything else.  Sorted by start, a
+// buffer must begin past the end of every written one before it, and a
+// written one past the end of every one before it.
+int check_written(std::vector<Span>& spans) {
+    const auto by_start = [](const Span& x, const Span& y) { return x.lo < y.lo; };
+    if (!std::is_sorted(spans.begin(), spans.end(), by_start)) std::sort(spans.begin(), spans.end(), by_start);
+    uintptr_t any = 0, written = 0;
+    for (const Span& s : spans) {
+        if (s.lo < written || (s.written && s.lo < any))
+            return fail(DDP_E_OVERLAP, "%s[%d] overlaps another buffer of the call", s.what, s.index);
+        any = std::max(any, s.hi);
+        if (s.written) written = std::max(written, s.hi);
+    }
+    return DDP_OK;
+}
+
+// Runs a call's body; host memory that runs out is a status, not an
+// exception through the C boundary.
+template <class F>
+int guarded(F body) {
+    try {
+        return body();
+    } catch (const std::bad_alloc&) {
+        return fail(DDP_E_ARG, "out of host memory");
+    } catch (const std::length_error&) {
+        return fail(DDP_E_ARG, "out of host memory");
+    }
+}
+
+int check_list(int32_t n_tensors, const int64_t* numels) {
+    if (n_tensors < 1) return fail(DDP_E_ARG, "n_tensors = %d, must be >= 1", n_tensors);
+    if (numels == nullptr) return fail(DDP_E_ARG, "numels is NULL");
+    for (int32_t t = 0; t < n_tensors; ++t)
+        if (const int s = check_length(numels[t], "numels[t]")) return s;
+    return DDP_OK;
+}
+
+// One tensor of a list: present and aligned to its elements unless empty.
+int check_tensor(const void* p, int64_t numel, int es, const char* what, int32_t t) {
+    if (numel == 0) return DDP_OK;
+    if (p == nullptr) return fail(DDP_E_ARG, "%s[%d] is NULL", what, t);
+    if (reinterpret_cast<uintptr_t>(p) % es)
+        return fail(DDP_E_ALIGN, "%s[%d] is not aligned to its element size", what, t);
+    return DDP_OK;
+}
+
+Span span_of(const void* p, int64_t bytes, bool written, const char* what, int32_t t) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + static_cast<uintptr_t>(bytes), written, what, t};
+}
+
+int check_norm_ptr(const float* norm) {
+    if (norm == nullptr) return fail(DDP_E_ARG, "norm is NULL");
+    if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(DDP_E_ALIGN, "norm is not 4-byte aligned");
+    return DDP_OK;
+}
+
+int check_workspace(const void* workspace, int64_t bytes, int64_t need) {
+    if (workspace == nullptr) return fail(DDP_E_ARG, "workspace is NULL");
+    if (bytes < need)
+        return fail(DDP_E_ARG, "workspace of %lld bytes, %lld needed", static_cast<long long>(bytes),
+                    static_cast<long long>(need));
+    if (reinterpret_cast<uintptr_t>(workspace) & 15u) return fail(DDP_E_ALIGN, "workspace is not 16-byte aligned");
+    return DDP_OK;
+}
+
+int check_max_norm(double max_norm) {
+    if (!(max_norm >= 0.0)) return fail(DDP_E_ARG, "max_norm = %g, must be >= 0", max_norm);
+    return DDP_OK;
+}
+
+// The norm (out == NULL) or the clipping of a list of tensors.
+int norm_or_clip(int32_t n_tensors, const int64_t* numels, const void* const* ptrs, const int32_t* dtypes,
+                 void* const* out, double max_norm, bool norm_given, float* norm, void* workspace,
+                 int64_t workspace_bytes, void* stream) {
+    int s = check_list(n_tensors, numels);
+    if (s) return s;
+    if (ptrs == nullptr || dtypes == nullptr) return fail(DDP_E_ARG, "NULL pointer argument");
+    if ((s = check_norm_ptr(norm))) return s;
+    if (!norm_given && (s = check_workspace(workspace, workspace_bytes, DDP_NORM_WORKSPACE_BYTES))) return s;
+    std::vector<Span> spans;
+    spans.reserve((out != nullptr ? 2 : 1) * static_cast<size_t>(n_tensors) + 2);
+    for (int32_t t = 0; t < n_tensors; ++t) {
+        if (!valid_dtype(dtypes[t])) return fail(DDP_E_ARG, "dtypes[%d] = %d is unknown", t, dtypes[t]);
+        const int es = elem_bytes(dtypes[t]);
+        if ((s = check_tensor(ptrs[t], numels[t], es, "ptrs", t))) return s;
+        if (out != nullptr && (s = check_tensor(out[t], numels[t], es, "out", t))) return s;
+        if (numels[t] == 0) continue;
+        const bool in_place = out != nullptr && out[t] == ptrs[t];
+        spans.push_back(span_of(ptrs[t], numels[t] * es, in_place, "ptrs", t));
+        if (out != nullptr && !in_place) spans.push_back(span_of(out[t], numels[t] * es, true, "out", t));
+    }
+    spans.push_back(span_of(norm, sizeof(float), !norm_given, "norm", 0));
+    if (!norm_given) spans.push_back(span_of(workspace, DDP_NORM_WORKSPACE_BYTES, true, "workspace", 0));
+    if ((s = check_written(spans))) return s;
+
+    ddp::NormLaunch l{};
+    l.n_tensors = n_tensors;
+    l.numels = numels;
+    l.in = ptrs;
+    l.dtypes = dtypes;
+    l.out = out;
+    l.partials = norm_given ? nullptr : static_cast<double*>(workspace);
+    l.norm = norm;
+    l.max_norm = static_cast<float>(max_norm);
+    l.stream = stream;
+    const char* msg = nullptr;
+    int partials = 0;
+    int e = norm_given ? 0 : ddp::launch_square_sums(l, &partials, &msg);
+    // The clipping kernel adds the partials itself; with no element at all
+    // there is no such launch.
+    if (e == 0 && !norm_given && (out == nullptr || partials == 0))
+        e = ddp::launch_norm_of(l.partials, partials, nullptr, norm, stream, &msg);
+    if (e == 0 && out != nullptr) e = ddp::launch_clip(l, partials, &msg);
+    if (e != 0) return hip_fail(e, msg);
+    return ok();
+}
+
+// Workgroups, and so partials, of an all-reduce with norm; the sum's
+// second level goes behind them.
+int64_t norm_workgroups(const ddp::RingLaunch& l, int64_t bucket_elems) {
+    if (bucket_elems == 0) return ddp::ring_workgroups(l);
+    int64_t sum = 0;
+    for (const BucketPart& p : bucket_parts(l, bucket_elems)) {
+        ddp::RingLaunch b = l;
+        b.n = p.count;
+        b.chunking = p.chunking;
+        b.seg2 = p.seg2;
+        b.seg2_chunking = p.seg2_chunking;
+        sum += ddp::ring_workgroups(b);
+    }
+    return sum;
+}
+
+int64_t norm_workspace(int64_t workgroups) {
+    const int64_t fold = workgroups > ddp::kNormFoldOver ? ddp::kNormFold : 0;
+    return (workgroups + fold) * static_cast<int64_t>(sizeof(double));
+}
+
+int ring_norm(ddp_reduce_op op, int32_t P, int32_t chunking, const void* const* rank_in, ddp_dtype in_dtype,
+              int32_t n_out, void* const* rank_out, ddp_dtype out_dtype, int64_t n, int64_t bucket_elems,
+              float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+    int s = validate_shape(op, P, chunking, in_dtype, out_dtype, n);
+    if (s) return s;
+    if (n_out != 1 && n_out != P) return fail(DDP_E_ARG, "n_out = %d, must be 1 or P", n_out);
+    if (bucket_elems != 0 && (s = check_bucket_elems(bucket_elems, in_dtype, out_dtype))) return s;
+    if ((s = check_norm_ptr(norm))) return s;
+    const char* msg = nullptr;
+    if (n == 0) {   // no element, no buffer to look at: the norm is 0
+        const int e = ddp::launch_norm_of(nullptr, 0, nullptr, norm, stream, &msg);
+        return e != 0 ? hip_fail(e, msg) : ok();
+    }
+    if ((s = check_ptr_array(rank_in, P, "rank_in"))) return s;
+    if ((s = check_ptr_array(const_cast<const void* const*>(rank_out), n_out, "rank_out"))) return s;
+
+    ddp::RingLaunch l{};
+    l.P = P;
+    l.chunking = chunking;
+    l.op = op;
+    l.in_bf16 = in_dtype == DDP_BF16;
+    l.out_bf16 = out_dtype == DDP_BF16;
+    l.write_out = 1;
+    for (int r = 0; r < P; ++r) l.in[r] = rank_in[r];
+    for (int r = 0; r < n_out; ++r) l.out[r] = rank_out[r];
+    l.n = n;
+    l.stream = stream;
+    l.one_copy = n_out == 1;
+    const int64_t groups = norm_workgroups(l, bucket_elems);
+    if ((s = check_workspace(workspace, workspace_bytes, norm_workspace(groups)))) return s;
+    std::vector<Buf> bufs;
+    add_rank_bufs(bufs, rank_in, P, n, elem_bytes(in_dtype), "rank_in");
+    add_rank_bufs(bufs, const_cast<const void* const*>(rank_out), n_out, n, elem_bytes(out_dtype), "rank_out");
+    if ((s = check_overlaps(bufs))) return s;
+    const Span nspan = span_of(norm, sizeof(float), true, "norm", 0);
+    const Span wspan = span_of(workspace, norm_workspace(groups), true, "workspace", 0);
+    for (const Span& x : {nspan, wspan})
+        for (const Buf& b : bufs)
+            if (x.lo < b.hi && b.lo < x.hi) return fail(DDP_E_OVERLAP, "%s overlaps %s[%d]", x.what, b.what, b.index);
+    if (nspan.lo < wspan.hi && wspan.lo < nspan.hi) return fail(DDP_E_OVERLAP, "norm overlaps workspace");
+
+    l.partials = static_cast<double*>(workspace);
+    int e = bucket_elems != 0 ? launch_buckets(l, bucket_elems, &msg) : ddp::launch_ring_reduce(l, &msg);
+    if (e == 0) e = ddp::launch_norm_of(l.partials, groups, l.partials + groups, norm, stream, &msg);
+    if (e != 0) return hip_fail(e, msg);
+    return ok();
+}
+
+int adamw_step(int32_t n_tensors, const int64_t* numels, const void* const* grads, ddp_dtype grad_dtype,
+               float* const* w, float* const* m, float* const* v, void* const* params, ddp_dtype param_dtype,
+               double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+               const int64_t* step_dev, const float* norm, double max_norm, void* stream) {
+    int s = check_list(n_tensors, numels);
+    if (s) return s;
+    if (!valid_dtype(grad_dtype) || !valid_dtype(param_dtype)) return fail(DDP_E_ARG, "unknown dtype");
+    if (grads == nullptr || w == nullptr || m == nullptr || v == nullptr)
+        return fail(DDP_E_ARG, "NULL pointer argument");
+    if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return fail(DDP_E_ARG, "lr and weight_decay must be finite");
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+        return fail(DDP_E_ARG, "beta1 = %g and beta2 = %g must be in [0, 1)", beta1, beta2);
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(DDP_E_ARG, "eps = %g, must be >= 0 and finite", eps);
+    if (step_dev == nullptr && step < 1)
+        return fail(DDP_E_ARG, "step = %lld, must be >= 1", static_cast<long long>(step));
+    if (reinterpret_cast<uintptr_t>(step_dev) % 8) return fail(DDP_E_ALIGN, "step_dev is not 8-byte aligned");
+    if (norm != nullptr && ((s = check_norm_ptr(norm)) || (s = check_max_norm(max_norm)))) return s;
+    const int ges = elem_bytes(grad_dtype);
+    const int pes = elem_bytes(param_dtype);
+    std::vector<Span> spans;
+    spans.reserve(5 * static_cast<size_t>(n_tensors) + 2);
+    // One stream after another: lists that lie in order in memory, each
+    // behind the one before, then need no sorting.
+    for (int32_t t = 0; t < n_tensors; ++t) {
+        if ((s = check_tensor(grads[t], numels[t], ges, "grads", t))) return s;
+        if (numels[t] > 0) spans.push_back(span_of(grads[t], numels[t] * ges, false, "grads", t));
+    }
+    const struct { float* const* list; const char* what; } state[3] = {{w, "w"}, {m, "m"}, {v, "v"}};
+    for (const auto& x : state) {
+        for (int32_t t = 0; t < n_tensors; ++t) {
+            if ((s = check_tensor(x.list[t], numels[t], 4, x.what, t))) return s;
+            if (numels[t] > 0) spans.push_back(span_of(x.list[t], numels[t] * 4, true, x.what, t));
+        }
+    }
+    for (int32_t t = 0; params != nullptr && t < n_tensors; ++t) {
+        if ((s = check_tensor(params[t], numels[t], pes, "params", t))) return s;
+        if (numels[t] > 0) spans.push_back(span_of(params[t], numels[t] * pes, true, "params", t));
+    }
+    if (norm != nullptr) spans.push_back(span_of(norm, sizeof(float), false, "norm", 0));
+    if (step_dev != nullptr) spans.push_back(span_of(step_dev, sizeof(int64_t), false, "step_dev", 0));
+    if ((s = check_written(spans))) return s;
+
+    ddp::AdamWLaunch l{};
+    l.n_tensors = n_tensors;
+    l.numels = numels;
+    l.grads = grads;
+    l.w = w;
+    l.m = m;
+    l.v = v;
+    l.params = params;
+    l.grad_bf16 = grad_dtype == DDP_BF16;
+    l.param_bf16 = param_dtype == DDP_BF16;
+    l.lr = lr;
+    l.beta1 = beta1;
+    l.beta2 = beta2;
+    l.eps = eps;
+    l.weight_decay = weight_decay;
+    l.step = step;
+    l.step_dev = step_dev;
+    l.norm = norm;
+    l.max_norm = static_cast<float>(norm != nullptr ? max_norm : 0.0);
+    l.stream = stream;
+    const char* msg = nullptr;
+    const int e = ddp::launch_adamw(l, &msg);
+    if (e != 0) return hip_fail(e, msg);
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int grad_norm_multi(int32_t n_tensors, const int64_t* numels, const void* const* ptrs, const int32_t* dtypes,
+                    void* workspace, int64_t workspace_bytes, float* norm, void* stream) {
+    return guarded([&] {
+        return norm_or_clip(n_tensors, numels, ptrs, dtypes, nullptr, 0.0, false, norm, workspace, workspace_bytes,
+                            stream);
+    });
+}
+
+int grad_clip_multi(int32_t n_tensors, const int64_t* numels, const void* const* ptrs, const int32_t* dtypes,
+                    void* const* out, double max_norm, int32_t norm_given, float* norm, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    if (out == nullptr) return fail(DDP_E_ARG, "out is NULL");
+    if (const int s = check_max_norm(max_norm)) return s;
+    return guarded([&] {
+        return norm_or_clip(n_tensors, numels, ptrs, dtypes, out, max_norm, norm_given != 0, norm, workspace,
+                            workspace_bytes, stream);
+    });
+}
+
+int allreduce_ring_norm(ddp_reduce_op op, int32_t P, int32_t chunking, const void* const* rank_in,
+                        ddp_dtype in_dtype, int32_t n_out, void* const* rank_out, ddp_dtype out_dtype, int64_t n,
+                        float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+    return guarded([&] {
+        return ring_norm(op, P, chunking, rank_in, in_dtype, n_out, rank_out, out_dtype, n, 0, norm, workspace,
+                         workspace_bytes, stream);
+    });
+}
+
+int allreduce_ring_norm_buckets(ddp_reduce_op op, int32_t P, int32_t chunking, const void* const* rank_in,
+                                ddp_dtype in_dtype, int32_t n_out, void* const* rank_out, ddp_dtype out_dtype,
+                                int64_t n, int64_t bucket_elems, float* norm, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+    if (bucket_elems == 0) return fail(DDP_E_ARG, "bucket_elems = 0, must be >= 1");
+    return guarded([&] {
+        return ring_norm(op, P, chunking, rank_in, in_dtype, n_out, rank_out, out_dtype, n, bucket_elems, norm,
+                         workspace, workspace_bytes, stream);
+    });
+}
+
+int allreduce_norm_workspace_bytes(int32_t P, int32_t chunking, ddp_dtype in_dtype, ddp_dtype out_dtype, int64_t n,
+                                   int64_t bucket_elems, int64_t* bytes) {
+    int s = check_ranks(P);
+    if (s) return s;
+    if (chunking < 1) return fail(DDP_E_ARG, "chunking = %d, must be >= 1", chunking);
+    if ((s = check_length(n, "n"))) return s;
+    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return fail(DDP_E_ARG, "unknown dtype");
+    if (bucket_elems != 0 && (s = check_bucket_elems(bucket_elems, in_dtype, out_dtype))) return s;
+    if (bytes == nullptr) return fail(DDP_E_ARG, "bytes is NULL");
+    ddp::RingLaunch l{};
+    l.P = P;
+    l.chunking = chunking;
+    l.in_bf16 = in_dtype == DDP_BF16;
+    l.out_bf16 = out_dtype == DDP_BF16;
+    l.n = n;
+    return guarded([&] {
+        *bytes = norm_workspace(norm_workgroups(l, bucket_elems));
+        return ok();
+    });
+}
+
+int adamw_step_multi(int32_t n_tensors, const int64_t* numels, const void* const* grads, ddp_dtype grad_dtype,
+                     float* const* w, float* const* m, float* const* v, void* const* params, ddp_dtype param_dtype,
+                     double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                     const int64_t* step_dev, const float* norm, double max_norm, void* stream) {
+    return guarded([&] {
+        return adamw_step(n_tensors, numels, grads, grad_dtype, w, m, v, params, param_dtype, lr, beta1, beta2, eps,
+                          weight_decay, step, step_dev, norm, max_norm, stream);
+    });
 }
 
 }  // extern "C"

@@ -1,0 +1,79 @@
+// grad_vec.h -- device helpers shared by the kernels that walk many gradient
+// tensors (grad_norm.hip, adamw.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ring_reduce_impl.h"
+
+namespace ddp {
+namespace gv {
+
+using rr::u32x2;
+using rr::u32x4;
+
+// Vectors at addresses aligned to the element only.  The hardware's vector
+// accesses take any alignment, so a tensor whose start differs from the
+// others' within 16 bytes needs no path of its own; aligned ones compile
+// to the same instruction.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+// Through global-address-space pointers: the tensors' addresses come out of
+// an argument table, where the compiler cannot tell that they are global.
+typedef __attribute__((address_space(1))) const u32x4_any* GlobalIn4;
+typedef __attribute__((address_space(1))) const u32x2_any* GlobalIn2;
+typedef __attribute__((address_space(1))) u32x4_any* GlobalOut4;
+typedef __attribute__((address_space(1))) u32x2_any* GlobalOut2;
+
+__device__ __forceinline__ u32x4 load4(const char* p) { return *(GlobalIn4)(p); }
+__device__ __forceinline__ u32x2 load2(const char* p) { return *(GlobalIn2)(p); }
+__device__ __forceinline__ u32x4 load4_nt(const char* p) { return __builtin_nontemporal_load((GlobalIn4)(p)); }
+__device__ __forceinline__ u32x2 load2_nt(const char* p) { return __builtin_nontemporal_load((GlobalIn2)(p)); }
+__device__ __forceinline__ void store4_nt(char* p, u32x4 v) { __builtin_nontemporal_store(v, (GlobalOut4)(p)); }
+__device__ __forceinline__ void store2_nt(char* p, u32x2 v) { __builtin_nontemporal_store(v, (GlobalOut2)(p)); }
+
+// One element as float32, and a float32 rounded to nearest even into one.
+template <bool BF16>
+__device__ __forceinline__ float load_elem(const char* p) {
+    if constexpr (BF16) {
+        return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
+    } else {
+        return *reinterpret_cast<const float*>(p);
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ void store_elem(char* p, float x) {
+    if constexpr (BF16) {
+        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(rr::bf16_bits(x));
+    } else {
+        *reinterpret_cast<float*>(p) = x;
+    }
+}
+
+// The clipping factor min(1, max_norm / (norm + 1e-6)) in float32, one
+// rounding per operation.  No limit (infinite max_norm) never scales; a
+// norm that is infinite gives 0 and one that is NaN gives NaN.
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+#pragma clang fp contract(off)
+    if (max_norm == __builtin_inff()) return 1.0f;
+    const float c = max_norm / (norm + 1e-6f);
+    return c > 1.0f ? 1.0f : c;
+}
+
+// Sum of `x` over the workgroup's waves in a fixed order, in every lane.
+template <int BLOCK>
+__device__ __forceinline__ double block_sum(double x) {
+    __shared__ double part[BLOCK / 64];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    __syncthreads();
+    double s = part[0];
+#pragma unroll
+    for (int w = 1; w < BLOCK / 64; ++w) s += part[w];
+    return s;
+}
+
+}  // namespace gv
+}  // namespace ddp

@@ -150,10 +150,18 @@ struct RingLaunch {
     // with seg2 a multiple of ring_tile_elems and whole chunks before it.
     int64_t seg2;
     int seg2_chunking;
+    // kAllReduce without sgd: where each workgroup leaves the sum of the
+    // squares it wrote (ring_workgroups of them), or null; and whether only
+    // rank 0 receives the result then.
+    double* partials;
+    int one_copy;
 };
 
 // Returns 0 on success, else a HIP error code; *msg names the failing call.
 int launch_ring_reduce(const RingLaunch& l, const char** msg);
+
+// Workgroups launch_ring_reduce starts for this launch, over all its parts.
+int64_t ring_workgroups(const RingLaunch& l);
 
 // Elements per workgroup tile of the vector ring kernel for this launch.
 int64_t ring_tile_elems(const RingLaunch& l);

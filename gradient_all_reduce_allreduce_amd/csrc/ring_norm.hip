@@ -1,0 +1,78 @@
+// ring_norm.hip -- the ring all-reduce that also leaves the sum of squares of
+// its result, for gfx950: the ring's tile code (ring_reduce_impl.h) with the
+// squares taken on the way.
+//
+// The global norm of the reduced gradient needs every element once more;
+// here its square is taken from the registers the result is stored from (as
+// it is written: rounded for bf16), in float64, where it is exact.  Each
+// workgroup -- one wave, one tile -- adds its lanes in a fixed order and
+// writes one partial; a second, small launch adds the partials
+// (grad_norm.hip).
+#include "ring_norm.h"
+
+namespace ddp {
+namespace rr {
+namespace {
+
+typedef const __attribute__((address_space(4))) RingNormArgs* KRingNorm;
+
+__device__ __forceinline__ KRingNorm norm_args() {
+    return (KRingNorm)(__builtin_amdgcn_kernarg_segment_ptr());
+}
+
+// The sum over the wave's lanes, in every lane.
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
+    return x;
+}
+
+template <int P, bool INB, bool OUTB>
+__global__ __launch_bounds__(kBlock) void ring_norm_kernel(RingNormArgs) {
+    const KRingNorm a = norm_args();
+    double sq = 0.0;
+    ring_reduce_body<P, INB, OUTB, false, true>(&sq, a->one_copy != 0);
+    sq = wave_sum(sq);
+    if (threadIdx.x == 0) a->partials[blockIdx.x] = sq;
+}
+
+template <int P, bool INB, bool OUTB>
+__global__ __launch_bounds__(kBlock) void ring_norm_scalar_kernel(RingNormArgs) {
+    const KRingNorm a = norm_args();
+    const uint32_t i = blockIdx.x * kBlock + threadIdx.x;
+    double sq = 0.0;
+    if (i < a->ring.n) process_element<P, INB, OUTB, false, true>(&a->ring, i, &sq, a->one_copy != 0);
+    sq = wave_sum(sq);
+    if (threadIdx.x == 0) a->partials[blockIdx.x] = sq;
+}
+
+template <bool INB, bool OUTB, bool SCALAR>
+const void* ring_norm_kernel_for(int P) {
+    switch (P) {
+#define DDP_CASE(p)                                                                                \
+    case p:                                                                                        \
+        return SCALAR ? reinterpret_cast<const void*>(&ring_norm_scalar_kernel<p, INB, OUTB>)      \
+                      : reinterpret_cast<const void*>(&ring_norm_kernel<p, INB, OUTB>);
+        DDP_CASE(1) DDP_CASE(2) DDP_CASE(3) DDP_CASE(4)
+        DDP_CASE(5) DDP_CASE(6) DDP_CASE(7) DDP_CASE(8)
+        DDP_CASE(9) DDP_CASE(10) DDP_CASE(11) DDP_CASE(12)
+        DDP_CASE(13) DDP_CASE(14) DDP_CASE(15) DDP_CASE(16)
+#undef DDP_CASE
+        default:
+            return nullptr;
+    }
+}
+
+}  // namespace
+}  // namespace rr
+
+const void* ring_norm_kernel(int P, bool in_bf16, bool out_bf16, int scalar) {
+    if (in_bf16) {
+        if (out_bf16) return scalar ? rr::ring_norm_kernel_for<true, true, true>(P) : rr::ring_norm_kernel_for<true, true, false>(P);
+        return scalar ? rr::ring_norm_kernel_for<true, false, true>(P) : rr::ring_norm_kernel_for<true, false, false>(P);
+    }
+    if (out_bf16) return scalar ? rr::ring_norm_kernel_for<false, true, true>(P) : rr::ring_norm_kernel_for<false, true, false>(P);
+    return scalar ? rr::ring_norm_kernel_for<false, false, true>(P) : rr::ring_norm_kernel_for<false, false, false>(P);
+}
+
+}  // namespace ddp

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "launch.h"
+#include "ring_norm.h"
 #include "ring_reduce_impl.h"
 
 namespace ddp {
@@ -22,6 +23,7 @@ const void* select_kernel(const RingLaunch& l, int scalar) {
             if (l.in_bf16) return l.out_bf16 ? tree_kernel_bf16_bf16(P, scalar) : tree_kernel_bf16_f32(P, scalar);
             return l.out_bf16 ? tree_kernel_f32_bf16(P, scalar) : tree_kernel_f32_f32(P, scalar);
         default:
+            if (l.partials != nullptr) return ring_norm_kernel(P, l.in_bf16 != 0, l.out_bf16 != 0, scalar);
             if (l.in_bf16) {
                 return l.out_bf16 ? ring_kernel_bf16_bf16(P, l.sgd, scalar) : ring_kernel_bf16_f32(P, l.sgd, scalar);
             }
@@ -81,7 +83,43 @@ int wg_per_cu(const RingLaunch& l) {
     }
 }
 
+// Workgroups of a launch over n elements.
+int64_t launch_grid(int64_t n, int64_t V, int64_t tile, int scalar) {
+    if (scalar) return (n + rr::kBlock - 1) / rr::kBlock;
+    const int64_t grid = (n - n % V + tile - 1) / tile;   // one tile per workgroup
+    return grid < 1 ? 1 : grid;                           // the tail still needs a workgroup
+}
+
+// Chunk lengths: the ring's; for the tree strategies those of a ring within
+// the nodes (*L) and over the nodes (*Lg), or a length beyond any index where
+// a level's order is fixed.
+void chunk_lengths(const RingLaunch& l, bool two, int64_t* L, int64_t* Lg) {
+    const int64_t kFixed = int64_t(1) << 62;
+    *Lg = kFixed;
+    if (l.mode == kTree) {
+        *L = l.local_chunking > 0 ? (l.n + l.local_chunking - 1) / l.local_chunking : kFixed;
+        *Lg = l.global_chunking > 0 ? (l.n + l.global_chunking - 1) / l.global_chunking : kFixed;
+    } else if (two) {
+        *L = (l.seg2 + l.chunking - 1) / l.chunking;
+        *Lg = (l.n - l.seg2 + l.seg2_chunking - 1) / l.seg2_chunking;
+    } else {
+        *L = (l.n + l.chunking - 1) / l.chunking;
+    }
+}
+
 }  // namespace
+
+int64_t ring_workgroups(const RingLaunch& l) {
+    if (l.n <= 0) return 0;
+    int64_t V = 4, tile = 0, L = 0, Lg = 0;
+    tile_shape(l, &V, &tile);
+    chunk_lengths(l, l.seg2 > 0 && l.seg2 < l.n, &L, &Lg);
+    const int scalar = (L < Lg ? L : Lg) < tile ? 1 : 0;
+    int64_t sum = 0;
+    for (int64_t base = 0; base < l.n; base += kMaxLaunchElems)
+        sum += launch_grid(l.n - base < kMaxLaunchElems ? l.n - base : kMaxLaunchElems, V, tile, scalar);
+    return sum;
+}
 
 int64_t ring_tile_elems(const RingLaunch& l) {
     int64_t V = 4, tile = 0;
@@ -102,21 +140,9 @@ int launch_ring_reduce(const RingLaunch& l, const char** msg) {
         *msg = "second segment not supported for this launch";
         return static_cast<int>(hipErrorInvalidValue);
     }
-    // Chunk lengths: the ring's; for the tree strategies those of a ring
-    // within the nodes (L) and over the nodes (Lg), or a length beyond any
-    // index where a level's order is fixed.
-    const int64_t kFixed = int64_t(1) << 62;
     const int groups = l.groups > 0 ? l.groups : 1;
-    int64_t L, Lg = kFixed;
-    if (l.mode == kTree) {
-        L = l.local_chunking > 0 ? (l.n + l.local_chunking - 1) / l.local_chunking : kFixed;
-        Lg = l.global_chunking > 0 ? (l.n + l.global_chunking - 1) / l.global_chunking : kFixed;
-    } else if (two) {
-        L = (l.seg2 + l.chunking - 1) / l.chunking;
-        Lg = (l.n - l.seg2 + l.seg2_chunking - 1) / l.seg2_chunking;
-    } else {
-        L = (l.n + l.chunking - 1) / l.chunking;
-    }
+    int64_t L = 0, Lg = 0;
+    chunk_lengths(l, two, &L, &Lg);
     // Chunks shorter than a tile would put several start ranks in one tile:
     // those calls use the one-element-per-lane kernels.
     const int scalar = (L < Lg ? L : Lg) < tile ? 1 : 0;
@@ -127,6 +153,7 @@ int launch_ring_reduce(const RingLaunch& l, const char** msg) {
     }
     const int ies = l.in_bf16 ? 2 : 4;
     const int oes = l.out_bf16 ? 2 : 4;
+    int64_t partials = 0;   // workgroups of the launches so far
 
     for (int64_t base = 0; base < l.n; base += kMaxLaunchElems) {
         const int64_t n = l.n - base < kMaxLaunchElems ? l.n - base : kMaxLaunchElems;
@@ -152,13 +179,7 @@ int launch_ring_reduce(const RingLaunch& l, const char** msg) {
         a.group_size = l.P / groups;
         a.seg2 = two ? static_cast<uint32_t>(l.seg2) : 0xffffffffu;
 
-        int64_t grid;
-        if (scalar) {
-            grid = (n + rr::kBlock - 1) / rr::kBlock;
-        } else {
-            grid = (a.n_vec + tile - 1) / tile;   // one tile per workgroup
-            if (grid < 1) grid = 1;               // the tail still needs a workgroup
-        }
+        const int64_t grid = launch_grid(n, V, tile, scalar);
         rr::TreeArgs ta{};
         void* args[] = {&a};
         if (l.mode == kTree) {
@@ -172,6 +193,14 @@ int launch_ring_reduce(const RingLaunch& l, const char** msg) {
                         ta.order_in[(sg * Lr + sl) * l.P + k] =
                             a.in[((sg + k / Lr) % groups) * Lr + (sl + k) % Lr];
             args[0] = &ta;
+        }
+        rr::RingNormArgs na{};
+        if (l.partials != nullptr) {
+            na.ring = a;
+            na.partials = l.partials + partials;
+            na.one_copy = l.one_copy;
+            partials += grid;
+            args[0] = &na;
         }
         const hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(rr::kBlock), args,
                                              lds_reserve(wg_per_cu(l)), static_cast<hipStream_t>(l.stream));

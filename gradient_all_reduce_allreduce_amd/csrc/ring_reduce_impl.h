@@ -163,6 +163,22 @@ __device__ __forceinline__ float mean_of(float s) {
     }
 }
 
+// The value the result has where it is written: rounded for bf16 outputs.
+template <bool OUTB>
+__device__ __forceinline__ float written(float g) {
+    if constexpr (OUTB) {
+        return __uint_as_float(bf16_bits(g) << 16);
+    } else {
+        return g;
+    }
+}
+
+// acc + x^2 in float64: the square of a float32 is exact there.
+__device__ __forceinline__ double square_to(double acc, float x) {
+    const double d = x;
+    return __builtin_fma(d, d, acc);
+}
+
 __device__ __forceinline__ void momentum_step(float g, float& w, float& v, float lr, float mu) {
 #pragma clang fp contract(off)
     float vn = mu * v;
@@ -317,8 +333,8 @@ __device__ __forceinline__ int ring_start_rank(KArgs a, uint32_t i) {
     return i < seg2 ? chunk_start<P>(i, a->ring) : chunk_start<P>(i - seg2, a->global);
 }
 
-template <int P, bool INB, bool OUTB, bool SGD>
-__device__ __forceinline__ void process_element(KArgs a, uint32_t i) {
+template <int P, bool INB, bool OUTB, bool SGD, bool NORM = false>
+__device__ __forceinline__ void process_element(KArgs a, uint32_t i, double* sq = nullptr, bool one_copy = false) {
 #pragma clang fp contract(off)
     const int s = ring_start_rank<P>(a, i);
     float g;
@@ -343,8 +359,12 @@ __device__ __forceinline__ void process_element(KArgs a, uint32_t i) {
         if (!a->write_out) return;
         if (a->write_out == 2) g = w;
     }
+    if constexpr (NORM) *sq = square_to(*sq, written<OUTB>(g));
 #pragma unroll
     for (int r = 0; r < P; ++r) {
+        if constexpr (NORM) {
+            if (r > 0 && one_copy) break;
+        }
         if constexpr (OUTB) {
             static_cast<uint16_t*>(a->out[r])[i] = static_cast<uint16_t>(bf16_bits(g));
         } else {
@@ -367,8 +387,11 @@ __device__ __forceinline__ u32x4 load_lane(const void* p) {
 
 // One tile = U rows of kBlock lane vectors of V elements per rank,
 // processed by one workgroup.  FULL: the whole tile lies below n_vec.
-template <int P, bool INB, bool OUTB, bool SGD, bool FULL>
-__device__ __forceinline__ void process_tile(KArgs a, uint32_t t0, int s0, uint32_t next) {
+// NORM: adds the squares of this lane's results to *sq; with one_copy only
+// rank 0 receives them.
+template <int P, bool INB, bool OUTB, bool SGD, bool FULL, bool NORM = false>
+__device__ __forceinline__ void process_tile(KArgs a, uint32_t t0, int s0, uint32_t next, double* sq = nullptr,
+                                             bool one_copy = false) {
 #pragma clang fp contract(off)
     constexpr int U = ring_vectors_per_lane(P, SGD);
     constexpr int V = ring_lane_elems(INB, OUTB, SGD);
@@ -420,7 +443,8 @@ __device__ __forceinline__ void process_tile(KArgs a, uint32_t t0, int s0, uint3
     const float lr = SGD ? a->lr : 0.0f;
     const float mu = SGD ? a->mu : 0.0f;
     char* dst[P];
-    rotated_outs<P>(a, store_rotation(P), dst);
+    // One copy: rank 0's, dst[0] without the rotation.
+    rotated_outs<P>(a, NORM && one_copy ? 0 : store_rotation(P), dst);
     pin_sgpr(n);
     pin_sgpr(mean_flag);
     if constexpr (SGD) {
@@ -471,24 +495,37 @@ __device__ __forceinline__ void process_tile(KArgs a, uint32_t t0, int s0, uint3
                 for (int e = 0; e < 4; ++e) g[e] = ws[u][e];
             }
         }
+        if constexpr (NORM) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) *sq = square_to(*sq, written<OUTB>(g[e]));
+        }
         if constexpr (OUTB && V == 8) {
             u32x4 o;
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[k] = bf16_bits(g[2 * k]) | (bf16_bits(g[2 * k + 1]) << 16);
 #pragma unroll
-            for (int q = 0; q < P; ++q) store16(dst[q], n * OES, i0 * OES, o);
+            for (int q = 0; q < P; ++q) {
+                if (NORM && q > 0 && one_copy) break;
+                store16(dst[q], n * OES, i0 * OES, o);
+            }
         } else if constexpr (OUTB) {
             u32x2 o;
 #pragma unroll
             for (int k = 0; k < 2; ++k) o[k] = bf16_bits(g[2 * k]) | (bf16_bits(g[2 * k + 1]) << 16);
 #pragma unroll
-            for (int q = 0; q < P; ++q) store8(dst[q], n * OES, i0 * OES, o);
+            for (int q = 0; q < P; ++q) {
+                if (NORM && q > 0 && one_copy) break;
+                store8(dst[q], n * OES, i0 * OES, o);
+            }
         } else {
             u32x4 o;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(g[e]);
 #pragma unroll
-            for (int q = 0; q < P; ++q) store16(dst[q], n * OES, i0 * OES, o);
+            for (int q = 0; q < P; ++q) {
+                if (NORM && q > 0 && one_copy) break;
+                store16(dst[q], n * OES, i0 * OES, o);
+            }
         }
     }
 }
@@ -496,8 +533,8 @@ __device__ __forceinline__ void process_tile(KArgs a, uint32_t t0, int s0, uint3
 // One tile per workgroup and as many workgroups as tiles: the hardware
 // dispatcher hands tiles to whichever CU is free, which balances the load
 // across CUs and XCDs better than fixed per-workgroup shares.
-template <int P, bool INB, bool OUTB, bool SGD>
-__global__ __launch_bounds__(kBlock) void ring_reduce_kernel(RingArgs) {
+template <int P, bool INB, bool OUTB, bool SGD, bool NORM = false>
+__device__ __forceinline__ void ring_reduce_body(double* sq = nullptr, bool one_copy = false) {
     constexpr uint32_t TILE =
         static_cast<uint32_t>(kBlock) * ring_vectors_per_lane(P, SGD) * ring_lane_elems(INB, OUTB, SGD);
     const KArgs a = kernel_args();
@@ -544,14 +581,19 @@ __global__ __launch_bounds__(kBlock) void ring_reduce_kernel(RingArgs) {
         s0 = static_cast<int>(((second ? gfirst : rfirst) + q) % static_cast<uint32_t>(P));
     }
     if (t0 + TILE <= n_vec) {
-        process_tile<P, INB, OUTB, SGD, true>(a, t0, s0, next);
+        process_tile<P, INB, OUTB, SGD, true, NORM>(a, t0, s0, next, sq, one_copy);
     } else if (t0 < n_vec) {
-        process_tile<P, INB, OUTB, SGD, false>(a, t0, s0, next);
+        process_tile<P, INB, OUTB, SGD, false, NORM>(a, t0, s0, next, sq, one_copy);
     }
     if (blockIdx.x == gridDim.x - 1) {
         const uint32_t i = n_vec + threadIdx.x;
-        if (i < a->n) process_element<P, INB, OUTB, SGD>(a, i);
+        if (i < a->n) process_element<P, INB, OUTB, SGD, NORM>(a, i, sq, one_copy);
     }
+}
+
+template <int P, bool INB, bool OUTB, bool SGD>
+__global__ __launch_bounds__(kBlock) void ring_reduce_kernel(RingArgs) {
+    ring_reduce_body<P, INB, OUTB, SGD>();
 }
 
 // Chunks shorter than a tile (C large against n): one element per lane.

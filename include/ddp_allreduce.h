@@ -798,9 +798,170 @@ int allreduce_multi_ring_noalloc(ddp_reduce_op op, int32_t P, int32_t chunking,
                                  void* const* out_ptrs, ddp_dtype out_dtype,
                                  void* stream);
 
+/* Bytes of workspace grad_norm_multi and grad_clip_multi need. */
+#define DDP_NORM_WORKSPACE_BYTES (1 << 14)
+
+/*
+ * grad_norm_multi -- the global 2-norm of many gradient tensors.
+ *
+ *     norm = sqrt(sum over tensors t and elements i of g_t[i]^2)
+ *
+ * what gradient clipping and the watch over a training run ask for after
+ * the all-reduce, when every replica holds the same gradients (CS336
+ * Lecture 8, "Data Parallelism (DDP)", step 4: each rank's local optimizer
+ * step).  Squares and sums are float64, where the square of a float32 is
+ * exact and cannot overflow or underflow; the root is rounded to float32
+ * once.  The order of the sums depends on the tensors' sizes, starts within a
+ * 128-byte line and order only, so the same tensors give the same bits.
+ * An infinite element gives an infinite norm, a NaN a NaN.
+ *
+ *   n_tensors    number of tensors, >= 1
+ *   numels       HOST array [n_tensors], elements of each, >= 0
+ *   ptrs         HOST array [n_tensors] of device pointers, each aligned to
+ *                its element size (NULL allowed where numels is 0)
+ *   dtypes       HOST array [n_tensors] of ddp_dtype: types may be mixed
+ *   workspace    device memory, 16-byte aligned, workspace_bytes >=
+ *                DDP_NORM_WORKSPACE_BYTES; its contents before do not matter
+ *                and after are undefined
+ *   norm         device pointer to one float, receives the norm
+ * Host arrays are read during the call only.  Two launches (more for over
+ * 380 tensors).  Calls that may run at the same time (on two streams, in
+ * two graphs) need a workspace each.
+ * Errors: DDP_E_ARG (counts, NULL pointers, dtypes, a workspace that is too
+ * small), DDP_E_ALIGN, DDP_E_OVERLAP (workspace or norm inside a tensor or
+ * each other), DDP_E_HIP.
+ */
+int grad_norm_multi(int32_t n_tensors, const int64_t* numels, const void* const* ptrs,
+                    const int32_t* dtypes, void* workspace, int64_t workspace_bytes,
+                    float* norm, void* stream);
+
+/*
+ * grad_clip_multi -- scale many gradient tensors so that their global
+ * 2-norm is at most max_norm.
+ *
+ *     c = min(1, max_norm / (norm + 1e-6));   out_t = c * g_t
+ *
+ * c in float32, one rounding per operation; the product is rounded to
+ * float32 and, for bf16 tensors, to nearest even bf16.  A norm that is
+ * infinite gives c = 0 and one that is NaN c = NaN, and the product follows
+ * IEEE (infinite elements become NaN); an infinite max_norm gives c = 1.
+ *
+ *   out          HOST array [n_tensors] of device pointers, the types of the
+ *                inputs; an output may be its own input (in place).  When every
+ *                output is and c = 1, nothing is written.
+ *   max_norm     >= 0, not NaN (rounded to float32)
+ *   norm_given   0: the norm of these tensors is computed first (as
+ *                grad_norm_multi does, the same bits) and written to *norm;
+ *                nonzero: *norm is read, the norm that another call left
+ *                (of more tensors than these, of another rank's copy)
+ *   workspace    as for grad_norm_multi; may be NULL when norm_given
+ *   other arguments as for grad_norm_multi
+ * Every output must be disjoint from every other buffer of the call, its own
+ * input apart; the same tensor listed twice is therefore refused in place.
+ * Errors: as for grad_norm_multi.
+ */
+int grad_clip_multi(int32_t n_tensors, const int64_t* numels, const void* const* ptrs,
+                    const int32_t* dtypes, void* const* out, double max_norm,
+                    int32_t norm_given, float* norm, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/*
+ * allreduce_ring_norm / allreduce_ring_norm_buckets -- the all-reduce of
+ * allreduce_ring_emulated / allreduce_ring_buckets, leaving also the global
+ * 2-norm of the reduced gradient.
+ *
+ * The results are theirs, bit for bit.  The norm is that of one rank's
+ * result as it is written (after Mean and, for bf16 outputs, after
+ * rounding), with the sums of grad_norm_multi (float64, rounded once); its
+ * squares are taken as the results are stored, so the gradients are not read
+ * again.
+ *
+ *   n_out        P: every rank receives the result; 1: only rank_out[0] is
+ *                written, one copy that stands for the identical replicas
+ *                (what an optimizer step on one copy of the master weights
+ *                reads next)
+ *   rank_out     host array [n_out]
+ *   norm         device pointer to one float, receives the norm
+ *   workspace    device memory, 16-byte aligned, of at least the bytes
+ *                allreduce_norm_workspace_bytes gives for these arguments
+ *   other arguments, layout and ownership as for the calls above; with n = 0
+ *   the norm is 0 and rank_in, rank_out and workspace are not looked at
+ * Calls that may run at the same time need a workspace each.
+ * Errors: those of the calls above, DDP_E_ARG for n_out neither 1 nor P, a
+ * NULL norm or a workspace that is too small, DDP_E_OVERLAP for a workspace
+ * or norm that overlaps another buffer.
+ */
+int allreduce_ring_norm(ddp_reduce_op op, int32_t P, int32_t chunking,
+                        const void* const* rank_in, ddp_dtype in_dtype, int32_t n_out,
+                        void* const* rank_out, ddp_dtype out_dtype, int64_t n, float* norm,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+int allreduce_ring_norm_buckets(ddp_reduce_op op, int32_t P, int32_t chunking,
+                                const void* const* rank_in, ddp_dtype in_dtype, int32_t n_out,
+                                void* const* rank_out, ddp_dtype out_dtype, int64_t n,
+                                int64_t bucket_elems, float* norm, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/*
+ * allreduce_norm_workspace_bytes -- host only: the workspace of the two calls
+ * above (bucket_elems = 0: of allreduce_ring_norm), in *bytes.  It grows
+ * with n: 8 bytes for 256 to 2,048 elements (8 for 64 when the ring's chunks
+ * are shorter than that).
+ * Errors: DDP_E_ARG, DDP_E_ALIGN, as for the calls.
+ */
+int allreduce_norm_workspace_bytes(int32_t P, int32_t chunking, ddp_dtype in_dtype,
+                                   ddp_dtype out_dtype, int64_t n, int64_t bucket_elems,
+                                   int64_t* bytes);
+
+/*
+ * adamw_step_multi -- one AdamW step (Adam with decoupled weight decay) on
+ * many tensors, the gradients clipped by a given norm on the way.
+ *
+ * The local optimizer step every replica takes on the reduced gradients
+ * (CS336 Lecture 8, "Data Parallelism (DDP)"), on float32 master weights
+ * with a copy in the model's type ("Distributed Training", Related,
+ * "Mixed-Precision Training").  With t the step's number and c as for
+ * grad_clip_multi (1 without a norm), per element in float32 with one
+ * rounding per operation:
+ *     g = c * g
+ *     m = beta1 * m + (1 - beta1) * g
+ *     v = beta2 * v + (1 - beta2) * (g * g)
+ *     w = w * (1 - lr * weight_decay) - s * (m / (sqrt(v) * r + eps))
+ * with 1 - beta1, 1 - beta2, 1 - lr * weight_decay, s = lr / (1 - beta1^t) and
+ * r = 1 / sqrt(1 - beta2^t) computed in float64 and rounded to float32 once.
+ * The gradients are not changed.  With a norm that is not finite the step is
+ * left out: w, m, v and params stay as they were (a loss that overflowed
+ * does not reach the weights).
+ *
+ *   numels       HOST array [n_tensors], elements of each, >= 0
+ *   grads        HOST array [n_tensors], elements of grad_dtype
+ *   w, m, v      HOST arrays [n_tensors] of pointers to float32 master weights
+ *                and moments, updated in place
+ *   params       HOST array [n_tensors] receiving the new weights as
+ *                param_dtype (bf16: nearest even), or NULL
+ *   lr, weight_decay  finite;  beta1, beta2 in [0, 1);  eps >= 0, finite
+ *   step         t >= 1, used when step_dev is NULL
+ *   step_dev     device pointer to t as one int64 (8-byte aligned), or NULL:
+ *                a captured step whose count the graph's owner advances.
+ *                A value below 1 leaves the step out.
+ *   norm         device pointer to the float32 norm, or NULL: no clipping
+ *   max_norm     >= 0, not NaN; read with norm only
+ * Tensors need only the alignment of their element type; whole 16-byte
+ * vectors of streams that start alike within 128 bytes are the fastest.
+ * Every w, m, v and params buffer must be disjoint from every other buffer of
+ * the call.
+ * Errors: DDP_E_ARG, DDP_E_ALIGN, DDP_E_OVERLAP, DDP_E_HIP.
+ */
+int adamw_step_multi(int32_t n_tensors, const int64_t* numels, const void* const* grads,
+                     ddp_dtype grad_dtype, float* const* w, float* const* m, float* const* v,
+                     void* const* params, ddp_dtype param_dtype, double lr, double beta1,
+                     double beta2, double eps, double weight_decay, int64_t step,
+                     const int64_t* step_dev, const float* norm, double max_norm,
+                     void* stream);
+
 /* Kernel families whose launch shape ddp_set_wg_per_cu can override. */
 typedef enum ddp_kernel_family {
-    DDP_KF_RING = 0,            /* allreduce_ring_emulated */
+    DDP_KF_RING = 0,            /* allreduce_ring_emulated, allreduce_ring_norm */
     DDP_KF_RING_SGD = 1,        /* allreduce_fused_sgd, zero1_sgd_step_emulated */
     DDP_KF_TREE = 2,            /* allreduce_tree_emulated, allreduce_hierarchical_emulated */
     DDP_KF_REDUCE_SCATTER = 3,  /* reducescatter_ring_emulated */

@@ -34,6 +34,7 @@ Modules:
     hierarchical -- the two-level (local / global) all-reduce
     zero    -- ZeRO stage 1: reduce-scatter, the owner's optimizer step,
                all-gather of the updated parameters
+    grads   -- the global gradient norm, clipping by it, the AdamW step
 
 Parity status of each function is stated in its module header.
 """
@@ -47,11 +48,13 @@ from .zero import zero1_sgd_step
 from .bf16 import bf16_bits_to_f32, f32_to_bf16_bits
 from .sgd import sgd_momentum
 from .bucket import bucket_plan, pack, unpack
+from .grads import adamw, adamw64, clip_factor, clip_factor64, grad_norm
 
 __all__ = [
     "SUM", "MEAN", "chunk_length", "chunk_owners", "chunk_start_ranks",
     "chunk_start_ranks_at", "ring_all_gather", "ring_allreduce", "ring_reduce_scatter",
     "ring_allreduce_sampled", "bf16_bits_to_f32", "f32_to_bf16_bits",
     "sgd_momentum", "bucket_plan", "pack", "unpack", "tree_allreduce", "tree_parents",
-    "hierarchical_allreduce", "zero1_sgd_step",
+    "hierarchical_allreduce", "zero1_sgd_step", "adamw", "adamw64", "clip_factor",
+    "clip_factor64", "grad_norm",
 ]
