@@ -19,7 +19,7 @@ from .api import (SUM, MEAN, F32, BF16, MAX_RANKS, DdpError, ddp_bucket_plan, dd
                   allreduce_ring_buckets, allreduce_fused_sgd_buckets, zero1_sgd_step_buckets,
                   ddp_buckets_launch_count, reducescatter_ring_buckets, allgather_ring_buckets,
                   allreduce_ring_stepwise_buckets, allreduce_hierarchical_buckets,
-                  NORM_WORKSPACE_BYTES, grad_norm_multi, grad_clip_multi, allreduce_ring_norm,
+                  NORM_WORKSPACE_BYTES, grad_norm_multi, grad_norm_workspace_bytes, grad_clip_multi, allreduce_ring_norm,
                   allreduce_ring_norm_buckets, allreduce_norm_workspace_bytes, adamw_step_multi,
                   MultiGrad, grad_norm, clip_grads, adamw_step, allreduce_norm)
 from .bucketer import GradBucketer
@@ -38,7 +38,7 @@ __all__ = [
     "allreduce_ring_buckets", "allreduce_fused_sgd_buckets", "zero1_sgd_step_buckets",
     "ddp_buckets_launch_count", "reducescatter_ring_buckets", "allgather_ring_buckets",
     "allreduce_ring_stepwise_buckets", "allreduce_hierarchical_buckets",
-    "NORM_WORKSPACE_BYTES", "grad_norm_multi", "grad_clip_multi", "allreduce_ring_norm",
+    "NORM_WORKSPACE_BYTES", "grad_norm_multi", "grad_norm_workspace_bytes", "grad_clip_multi", "allreduce_ring_norm",
     "allreduce_ring_norm_buckets", "allreduce_norm_workspace_bytes", "adamw_step_multi",
     "MultiGrad", "grad_norm", "clip_grads", "adamw_step", "allreduce_norm",
 ]

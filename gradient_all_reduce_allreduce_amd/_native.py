@@ -29,7 +29,7 @@ DDP_MEAN = 1
 DDP_F32 = 0
 DDP_BF16 = 1
 DDP_MAX_RANKS = 16
-DDP_NORM_WORKSPACE_BYTES = 1 << 14
+DDP_NORM_WORKSPACE_BYTES = 1 << 13
 
 # ddp_kernel_family
 KERNEL_FAMILIES = {"ring": 0, "ring_sgd": 1, "tree": 2, "reduce_scatter": 3, "all_gather": 4,
@@ -139,6 +139,8 @@ _SIGNATURES = {
     "grad_norm_multi": (ctypes.c_int, [
         ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "grad_norm_workspace_bytes": (ctypes.c_int, [
+        ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
     "grad_clip_multi": (ctypes.c_int, [
         ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_double, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,

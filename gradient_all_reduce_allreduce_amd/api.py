@@ -14,7 +14,7 @@ Python ints, stream as an int handle or None):
     allreduce_hierarchical_emulated, ddp_multi_plan, ddp_multi_block_map, allreduce_multi_ring_emulated,
     allreduce_multi_fused_sgd, allreduce_multi_ring_noalloc, grad_norm_multi, grad_clip_multi,
     allreduce_ring_norm, allreduce_ring_norm_buckets, allreduce_norm_workspace_bytes,
-    adamw_step_multi, ddp_set_wg_per_cu
+    adamw_step_multi, grad_norm_workspace_bytes, ddp_set_wg_per_cu
 Tensor-level helpers:
     allreduce(tensors, op, chunking, out)            -> list of outputs
     allreduce_sgd(grads, w, v, lr, mu, op, chunking, out)
@@ -26,7 +26,6 @@ Tensor-level helpers:
     MultiGrad(grads)
 """
 
-import contextlib
 import ctypes
 
 import numpy as np
@@ -322,12 +321,22 @@ def _int_array(values):
 
 def grad_norm_multi(numels, ptrs, dtypes, workspace, workspace_bytes, norm, stream=None):
     """The global 2-norm of tensors given by host lists: T element counts,
-    device addresses and dtype codes.  ``workspace`` (device, at least
-    NORM_WORKSPACE_BYTES) and ``norm`` (one float) are device addresses."""
+    device addresses and dtype codes.  ``workspace`` (device, of
+    grad_norm_workspace_bytes) and ``norm`` (one float) are device addresses."""
     if not len(numels) == len(ptrs) == len(dtypes):
         raise ValueError("numels, ptrs and dtypes must have one entry per tensor")
     _check(N.lib().grad_norm_multi(len(numels), _long_array(numels), N.pointer_array(ptrs), _int_array(dtypes),
                                    workspace, workspace_bytes, norm, stream))
+
+
+def grad_norm_workspace_bytes(numels, dtypes, clip=False):
+    """Workspace of grad_norm_multi, or grad_clip_multi (host only)."""
+    if len(numels) != len(dtypes):
+        raise ValueError("numels and dtypes must have one entry per tensor")
+    b = ctypes.c_int64(0)
+    _check(N.lib().grad_norm_workspace_bytes(len(numels), _long_array(numels), _int_array(dtypes), int(bool(clip)),
+                                             ctypes.byref(b)))
+    return b.value
 
 
 def grad_clip_multi(numels, ptrs, dtypes, out, max_norm, norm_given, norm, workspace, workspace_bytes,
@@ -793,20 +802,15 @@ def allreduce_sgd(grads, w, v, lr, mu, op="mean", chunking=None, out=None, bucke
 
 # ------------------------------------------- norm, clipping, AdamW --------
 
-@contextlib.contextmanager
-def _other_device(device):
+def _on_device(index, call):
+    """``call(stream)`` with GPU ``index`` current (a launch on its default
+    stream, which names no device, must find it so) and the handle of that
+    GPU's current stream."""
     import torch
-    with torch.cuda.device(device):
-        yield
-
-
-def _on(device):
-    """A context in which ``device`` is current: launches on its default
-    stream, which has no device of its own, go there too."""
-    import torch
-    if device.index is None or torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return _other_device(device)
+    if torch.cuda.current_device() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _tensor_list(tensors, what, dtypes):
@@ -849,9 +853,12 @@ class MultiGrad:
         import torch
         self.grads = _tensor_list(grads, "MultiGrad", (torch.float32, torch.bfloat16))
         self.device = self.grads[0].device
-        self._numels = _long_array([g.numel() for g in self.grads])
-        self._ptrs = N.pointer_array([g.data_ptr() for g in self.grads])
-        self._dtypes = _int_array([torch_dtype_code(g.dtype) for g in self.grads])
+        numels = [g.numel() for g in self.grads]
+        codes = [torch_dtype_code(g.dtype) for g in self.grads]
+        self._list = (len(numels), _long_array(numels), N.pointer_array([g.data_ptr() for g in self.grads]),
+                      _int_array(codes))
+        self._norm_bytes = grad_norm_workspace_bytes(numels, codes)
+        self._clip_bytes = grad_norm_workspace_bytes(numels, codes, True)
 
     def _match(self, tensors, what, dtypes):
         """Tensors of the gradients' sizes, one each, on their device."""
@@ -861,19 +868,17 @@ class MultiGrad:
             raise ValueError(f"{what}: need one tensor of each gradient's size on its device")
         return tensors, N.pointer_array([x.data_ptr() for x in tensors])
 
-    def _workspace(self):
-        import torch
-        return torch.empty(NORM_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
-
     def norm(self):
         """The global 2-norm of all gradients, a float32 scalar tensor."""
         import torch
-        with _on(self.device):
-            ws = self._workspace()
+
+        def call(stream):
             norm = torch.empty((), dtype=torch.float32, device=self.device)
-            _check(N.lib().grad_norm_multi(len(self.grads), self._numels, self._ptrs, self._dtypes, ws.data_ptr(),
-                                           NORM_WORKSPACE_BYTES, norm.data_ptr(), current_stream(self.device)))
-        return norm
+            ws = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device) if self._norm_bytes else None
+            _check(N.lib().grad_norm_multi(*self._list, ws.data_ptr() if ws is not None else None, self._norm_bytes,
+                                           norm.data_ptr(), stream))
+            return norm
+        return _on_device(self.device.index, call)
 
     def bind_clip(self, out=None):
         """Returns ``run(max_norm, norm=None)``, which scales every gradient
@@ -883,27 +888,25 @@ class MultiGrad:
         (a float32 scalar tensor, e.g. of ``allreduce_norm``)."""
         import torch
         if out is None:
-            out, optrs = self.grads, self._ptrs
+            out, optrs = self.grads, self._list[2]
         else:
             out, optrs = self._match(out, "clip out", (torch.float32, torch.bfloat16))
             if any(o.dtype != g.dtype for o, g in zip(out, self.grads)):
                 raise ValueError("clip out: every output must have its gradient's type")
 
         def run(max_norm, norm=None):
-            given = norm is not None
-            with _on(self.device):
-                ws = None
-                if given:
-                    _scalar(norm, torch.float32, self.device, "norm")
-                else:
-                    norm = torch.empty((), dtype=torch.float32, device=self.device)
-                    ws = self._workspace()
-                _check(N.lib().grad_clip_multi(len(self.grads), self._numels, self._ptrs, self._dtypes, optrs,
-                                               max_norm, given, norm.data_ptr(),
-                                               ws.data_ptr() if ws is not None else None,
-                                               NORM_WORKSPACE_BYTES if ws is not None else 0,
-                                               current_stream(self.device)))
-            return norm
+            def call(stream):
+                result, ws = norm, None
+                if norm is None:
+                    result = torch.empty((), dtype=torch.float32, device=self.device)
+                    if self._clip_bytes:
+                        ws = torch.empty(self._clip_bytes, dtype=torch.uint8, device=self.device)
+                _check(N.lib().grad_clip_multi(*self._list, optrs, max_norm, norm is not None, result.data_ptr(),
+                                               ws.data_ptr() if ws is not None else None, self._clip_bytes, stream))
+                return result
+            if norm is not None:
+                _scalar(norm, torch.float32, self.device, "norm")
+            return _on_device(self.device.index, call)
 
         run.tensors = (self.grads, out)
         return run
@@ -926,6 +929,7 @@ class MultiGrad:
         w, wptrs = self._match(w, "adamw w", (torch.float32,))
         m, mptrs = self._match(m, "adamw m", (torch.float32,))
         v, vptrs = self._match(v, "adamw v", (torch.float32,))
+        count, numels, ptrs, _ = self._list
         pptrs, pcode = None, F32
         if params is not None:
             params, pptrs = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
@@ -942,11 +946,9 @@ class MultiGrad:
                 step = 0
             if norm is not None:
                 norm = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
-            with _on(self.device):
-                _check(N.lib().adamw_step_multi(len(self.grads), self._numels, self._ptrs, gcode, wptrs, mptrs,
-                                                vptrs, pptrs, pcode, lr, betas[0], betas[1], eps, weight_decay,
-                                                step, step_dev, norm, max_norm if norm is not None else 0.0,
-                                                current_stream(self.device)))
+            _on_device(self.device.index, lambda stream: _check(N.lib().adamw_step_multi(
+                count, numels, ptrs, gcode, wptrs, mptrs, vptrs, pptrs, pcode, lr, betas[0], betas[1], eps,
+                weight_decay, step, step_dev, norm, max_norm if norm is not None else 0.0, stream)))
 
         run.tensors = (self.grads, w, m, v, params)
         return run
@@ -994,13 +996,15 @@ def allreduce_norm(tensors, op="sum", chunking=None, out=None, out_dtype=None, b
     if bucket_elems is not None and bucket_elems < 1:
         raise ValueError("allreduce_norm: bucket_elems must be at least 1")
     need = allreduce_norm_workspace_bytes(P, C, icode, ocode, n, bucket_elems or 0)
-    with _on(device):
+    ins, outs = [t.data_ptr() for t in tensors], [t.data_ptr() for t in out]
+
+    def call(stream):
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         norm = torch.empty((), dtype=torch.float32, device=device)
-        ins, outs = [t.data_ptr() for t in tensors], [t.data_ptr() for t in out]
-        end = (norm.data_ptr(), ws.data_ptr(), need, current_stream(device))
+        end = (norm.data_ptr(), ws.data_ptr(), need, stream)
         if bucket_elems is not None:
             allreduce_ring_norm_buckets(op, P, C, ins, icode, outs, ocode, n, bucket_elems, *end)
         else:
             allreduce_ring_norm(op, P, C, ins, icode, outs, ocode, n, *end)
-    return out, norm
+        return out, norm
+    return _on_device(device.index, call)

@@ -27,7 +27,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <cmath>
 
 #include "grad_vec.h"
 #include "launch_grads.h"
@@ -38,23 +37,26 @@ namespace {
 using rr::u32x2;
 using rr::u32x4;
 
-constexpr int kBlock = 256;
-constexpr int kVecPerLane = 2;
-constexpr uint32_t kTileElems = kBlock * kVecPerLane * 4;
+constexpr int kBlock = 64;                             // one wave
+constexpr uint32_t kTileElems = kBlock * 4;
 constexpr uint32_t kLineElems = 32;                    // float32 per 128-byte line
-constexpr int64_t kMaxTiles = int64_t(1) << 30;
-constexpr int kCap = 144;                              // tensors per launch
-constexpr int kMaxGrid = 2048;
+// Tensors per launch: as many as the arguments hold, or few, whose arguments
+// are quicker to hand over.
+constexpr int kManyTensors = 144;
+constexpr int kFewTensors = 16;
 
+template <int CAP>
 struct AdamWArgs {
-    const char* g[kCap];
-    char* w[kCap];
-    char* m[kCap];
-    char* v[kCap];
-    char* p[kCap];
-    uint64_t numel[kCap];
-    uint32_t first_tile[kCap + 1];
+    static constexpr int kCap = CAP;
+    const char* g[CAP];
+    char* w[CAP];
+    char* m[CAP];
+    char* v[CAP];
+    char* p[CAP];
+    uint64_t numel[CAP];
+    uint32_t first_tile[CAP];
     int32_t n;
+    uint32_t tiles;          // of all tensors
     const float* norm;
     const int64_t* step;     // device; null: step_size and root2 hold the step's
     double b1, b2, lr;       // with `step`
@@ -66,17 +68,26 @@ struct AdamWArgs {
     float step_size;
     float root2;
 };
-static_assert(sizeof(AdamWArgs) <= 7800, "kernel arguments must stay under the 8,000 bytes measured to pass");
-typedef const __attribute__((address_space(4))) AdamWArgs* KAdamW;
+static_assert(sizeof(AdamWArgs<kManyTensors>) <= 7800, "kernel arguments must stay under the 8,000 bytes measured to pass");
+template <int CAP>
+using KAdamW = const __attribute__((address_space(4))) AdamWArgs<CAP>*;
 
-// b^t for t >= 1, float64, by squaring.
-__host__ __device__ __forceinline__ double power(double b, int64_t t) {
-    double r = 1.0;
+// What depends on the step's number: lr / (1 - b1^t) and 1 / sqrt(1 - b2^t),
+// the powers by squaring, all float64, rounded to float32 once.
+struct StepFactors {
+    float size, root2;
+};
+__host__ __device__ __forceinline__ StepFactors step_factors(double lr, double b1, double b2, int64_t t) {
+    double p1 = 1.0, p2 = 1.0;
     for (; t > 0; t >>= 1) {
-        if (t & 1) r *= b;
-        b *= b;
+        if (t & 1) {
+            p1 *= b1;
+            p2 *= b2;
+        }
+        b1 *= b1;
+        b2 *= b2;
     }
-    return r;
+    return {static_cast<float>(lr / (1.0 - p1)), static_cast<float>(1.0 / __builtin_sqrt(1.0 - p2))};
 }
 
 struct Factors {
@@ -101,25 +112,22 @@ __device__ __forceinline__ void adamw_element(float g, float& w, float& m, float
     w = w0 - s;
 }
 
-template <bool GB, int PM>   // bf16 gradients; copy: 0 none, 1 float32, 2 bf16
-__global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs) {
-    const KAdamW a = (KAdamW)(__builtin_amdgcn_kernarg_segment_ptr());
-    constexpr uint32_t GES = GB ? 2 : 4;
-    constexpr uint32_t PES = PM == 2 ? 2 : 4;
-    Factors f;
+// The factors from the arguments and the norm and step count they point to.
+// False: the step is left out.
+template <int CAP>
+__device__ __forceinline__ bool factors(KAdamW<CAP> a, float norm, int64_t t, Factors& f) {
     f.c = 1.0f;
     if (a->norm != nullptr) {
-        const float norm = *a->norm;
-        if (!(__builtin_fabsf(norm) < __builtin_inff())) return;
+        if (!(__builtin_fabsf(norm) < __builtin_inff())) return false;
         f.c = gv::clip_factor(norm, a->max_norm);
     }
     f.step_size = a->step_size;
     f.root2 = a->root2;
     if (a->step != nullptr) {
-        const int64_t t = *a->step;
-        if (t < 1) return;
-        f.step_size = static_cast<float>(a->lr / (1.0 - power(a->b1, t)));
-        f.root2 = static_cast<float>(1.0 / __builtin_sqrt(1.0 - power(a->b2, t)));
+        if (t < 1) return false;
+        const StepFactors s = step_factors(a->lr, a->b1, a->b2, t);
+        f.step_size = s.size;
+        f.root2 = s.root2;
     }
     f.beta1 = a->beta1;
     f.beta2 = a->beta2;
@@ -127,17 +135,24 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs) {
     f.one_beta2 = a->one_beta2;
     f.decay = a->decay;
     f.eps = a->eps;
+    return true;
+}
 
-    const uint64_t tiles = a->first_tile[a->n];
-    const uint32_t first = static_cast<uint32_t>(tiles * blockIdx.x / gridDim.x);
-    const uint32_t last = static_cast<uint32_t>(tiles * (blockIdx.x + 1) / gridDim.x);
-    int t = 0;
-    for (int h = a->n - 1; t < h;) {
-        const int mid = (t + h + 1) >> 1;
-        if (a->first_tile[mid] <= first) t = mid; else h = mid - 1;
-    }
-    for (uint32_t tile = first; tile < last; ++tile) {
-        while (tile >= a->first_tile[t + 1]) ++t;
+// GB: bf16 gradients.  PM: the copy, 0 none, 1 float32, 2 bf16.
+template <int CAP, bool GB, int PM>
+__global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs<CAP>) {
+    const KAdamW<CAP> a = (KAdamW<CAP>)(__builtin_amdgcn_kernarg_segment_ptr());
+    constexpr uint32_t GES = GB ? 2 : 4;
+    constexpr uint32_t PES = PM == 2 ? 2 : 4;
+    const uint32_t tiles = a->tiles;
+    const float norm = a->norm != nullptr ? gv::load_uniform(a->norm) : 0.0f;
+    const int64_t step = a->step != nullptr ? gv::load_uniform(a->step) : 1;
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        int t = 0;
+        for (int h = a->n - 1; t < h;) {
+            const int mid = (t + h + 1) >> 1;
+            if (a->first_tile[mid] <= tile) t = mid; else h = mid - 1;
+        }
         const char* const g = a->g[t];
         char* const w = a->w[t];
         char* const m = a->m[t];
@@ -146,46 +161,44 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs) {
         const int64_t n = static_cast<int64_t>(a->numel[t]);
         const int64_t lead = static_cast<int64_t>((reinterpret_cast<uint64_t>(w) >> 2) % kLineElems);
         const int64_t at = static_cast<int64_t>(tile - a->first_tile[t]) * kTileElems - lead;
+        Factors f;
         if (at >= 0 && at + kTileElems <= n) {
-            u32x4 gq[kVecPerLane], wq[kVecPerLane], mq[kVecPerLane], vq[kVecPerLane];
-#pragma unroll
-            for (int u = 0; u < kVecPerLane; ++u) {
-                const int64_t i = at + (u * kBlock + threadIdx.x) * 4;
-                if constexpr (GB) {
-                    const u32x2 h = gv::load2_nt(g + i * 2);
-                    gq[u] = u32x4{h[0], h[1], 0u, 0u};
-                } else {
-                    gq[u] = gv::load4_nt(g + i * 4);
-                }
-                wq[u] = gv::load4_nt(w + i * 4);
-                mq[u] = gv::load4_nt(m + i * 4);
-                vq[u] = gv::load4_nt(v + i * 4);
+            const int64_t i = at + threadIdx.x * 4;
+            u32x4 gq;
+            if constexpr (GB) {
+                const u32x2 h = gv::load2_nt(g + i * 2);
+                gq = u32x4{h[0], h[1], 0u, 0u};
+            } else {
+                gq = gv::load4_nt(g + i * 4);
             }
+            u32x4 wq = gv::load4_nt(w + i * 4);
+            u32x4 mq = gv::load4_nt(m + i * 4);
+            u32x4 vq = gv::load4_nt(v + i * 4);
+            // The factors (divisions, two powers) while the tile's data is in
+            // flight.
+            if (!factors(a, norm, step, f)) return;
+            float wn[4];
 #pragma unroll
-            for (int u = 0; u < kVecPerLane; ++u) {
-                const int64_t i = at + (u * kBlock + threadIdx.x) * 4;
-                float wn[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float me = __uint_as_float(mq[u][e]);
-                    float ve = __uint_as_float(vq[u][e]);
-                    wn[e] = __uint_as_float(wq[u][e]);
-                    adamw_element(rr::elem<GB>(gq[u], e), wn[e], me, ve, f);
-                    wq[u][e] = __float_as_uint(wn[e]);
-                    mq[u][e] = __float_as_uint(me);
-                    vq[u][e] = __float_as_uint(ve);
-                }
-                gv::store4_nt(w + i * 4, wq[u]);
-                gv::store4_nt(m + i * 4, mq[u]);
-                gv::store4_nt(v + i * 4, vq[u]);
-                if constexpr (PM == 1) gv::store4_nt(p + i * 4, wq[u]);
-                if constexpr (PM == 2)
-                    gv::store2_nt(p + i * 2, u32x2{rr::bf16_bits(wn[0]) | (rr::bf16_bits(wn[1]) << 16),
-                                                   rr::bf16_bits(wn[2]) | (rr::bf16_bits(wn[3]) << 16)});
+            for (int e = 0; e < 4; ++e) {
+                float me = __uint_as_float(mq[e]);
+                float ve = __uint_as_float(vq[e]);
+                wn[e] = __uint_as_float(wq[e]);
+                adamw_element(rr::elem<GB>(gq, e), wn[e], me, ve, f);
+                wq[e] = __float_as_uint(wn[e]);
+                mq[e] = __float_as_uint(me);
+                vq[e] = __float_as_uint(ve);
             }
+            gv::store4_nt(w + i * 4, wq);
+            gv::store4_nt(m + i * 4, mq);
+            gv::store4_nt(v + i * 4, vq);
+            if constexpr (PM == 1) gv::store4_nt(p + i * 4, wq);
+            if constexpr (PM == 2)
+                gv::store2_nt(p + i * 2, u32x2{rr::bf16_bits(wn[0]) | (rr::bf16_bits(wn[1]) << 16),
+                                               rr::bf16_bits(wn[2]) | (rr::bf16_bits(wn[3]) << 16)});
             continue;
         }
         // A tensor's first or last tile: one element per lane.
+        if (!factors(a, norm, step, f)) return;
         const int64_t lo = at < 0 ? 0 : at;
         const int64_t hi = at + kTileElems < n ? at + kTileElems : n;
         for (int64_t i = lo + threadIdx.x; i < hi; i += kBlock) {
@@ -202,22 +215,22 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs) {
     }
 }
 
+template <int CAP>
 const void* kernel_for(const AdamWLaunch& l) {
     const int pm = l.params == nullptr ? 0 : (l.param_bf16 ? 2 : 1);
     if (l.grad_bf16) {
-        return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<true, 0>)
-               : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<true, 1>)
-                         : reinterpret_cast<const void*>(&adamw_kernel<true, 2>);
+        return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, true, 0>)
+               : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, true, 1>)
+                         : reinterpret_cast<const void*>(&adamw_kernel<CAP, true, 2>);
     }
-    return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<false, 0>)
-           : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<false, 1>)
-                     : reinterpret_cast<const void*>(&adamw_kernel<false, 2>);
+    return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, false, 0>)
+           : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, false, 1>)
+                     : reinterpret_cast<const void*>(&adamw_kernel<CAP, false, 2>);
 }
 
-}  // namespace
-
-int launch_adamw(const AdamWLaunch& l, const char** msg) {
-    AdamWArgs a;
+template <int CAP>
+int launch_all(const AdamWLaunch& l, const char** msg) {
+    AdamWArgs<CAP> a;
     a.norm = l.norm;
     a.max_norm = l.max_norm;
     a.step = l.step_dev;
@@ -233,14 +246,15 @@ int launch_adamw(const AdamWLaunch& l, const char** msg) {
     a.step_size = 0.0f;
     a.root2 = 0.0f;
     if (l.step_dev == nullptr) {
-        a.step_size = static_cast<float>(l.lr / (1.0 - power(l.beta1, l.step)));
-        a.root2 = static_cast<float>(1.0 / std::sqrt(1.0 - power(l.beta2, l.step)));
+        const StepFactors s = step_factors(l.lr, l.beta1, l.beta2, l.step);
+        a.step_size = s.size;
+        a.root2 = s.root2;
     }
-    const void* fn = kernel_for(l);
+    const void* fn = kernel_for<CAP>(l);
     for (int32_t t = 0; t < l.n_tensors;) {
         int64_t tiles = 0;
         a.n = 0;
-        for (; t < l.n_tensors && a.n < kCap; ++t) {
+        for (; t < l.n_tensors && a.n < CAP; ++t) {
             const int64_t n = l.numels[t];
             if (n == 0) continue;
             const int64_t lead = static_cast<int64_t>((reinterpret_cast<uintptr_t>(l.w[t]) >> 2) % kLineElems);
@@ -257,16 +271,23 @@ int launch_adamw(const AdamWLaunch& l, const char** msg) {
             ++a.n;
         }
         if (a.n == 0) continue;
-        a.first_tile[a.n] = static_cast<uint32_t>(tiles);
-        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, kMaxGrid));
+        a.tiles = static_cast<uint32_t>(tiles);
+        const unsigned grid = std::min(a.tiles, kMaxWaveGrid);
         void* args[] = {&a};
-        const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kBlock), args, 0, static_cast<hipStream_t>(l.stream));
+        const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kBlock), args, lds_reserve(kAdamWWgPerCu),
+                                             static_cast<hipStream_t>(l.stream));
         if (e != hipSuccess) {
             *msg = "hipLaunchKernel(adamw)";
             return static_cast<int>(e);
         }
     }
     return 0;
+}
+
+}  // namespace
+
+int launch_adamw(const AdamWLaunch& l, const char** msg) {
+    return l.n_tensors <= kFewTensors ? launch_all<kFewTensors>(l, msg) : launch_all<kManyTensors>(l, msg);
 }
 
 }  // namespace ddp

@@ -1367,8 +1367,12 @@ int guarded(F body) {
 int check_list(int32_t n_tensors, const int64_t* numels) {
     if (n_tensors < 1) return fail(DDP_E_ARG, "n_tensors = %d, must be >= 1", n_tensors);
     if (numels == nullptr) return fail(DDP_E_ARG, "numels is NULL");
-    for (int32_t t = 0; t < n_tensors; ++t)
+    for (int32_t t = 0; t < n_tensors; ++t) {
         if (const int s = check_length(numels[t], "numels[t]")) return s;
+        if (numels[t] > ddp::kMaxGradElems)
+            return fail(DDP_E_UNSUPPORTED, "numels[%d] = %lld is over 2^36 elements", t,
+                        static_cast<long long>(numels[t]));
+    }
     return DDP_OK;
 }
 
@@ -1406,19 +1410,27 @@ int check_max_norm(double max_norm) {
     return DDP_OK;
 }
 
+int check_dtypes(int32_t n_tensors, const int32_t* dtypes) {
+    if (dtypes == nullptr) return fail(DDP_E_ARG, "dtypes is NULL");
+    for (int32_t t = 0; t < n_tensors; ++t)
+        if (!valid_dtype(dtypes[t])) return fail(DDP_E_ARG, "dtypes[%d] = %d is unknown", t, dtypes[t]);
+    return DDP_OK;
+}
+
 // The norm (out == NULL) or the clipping of a list of tensors.
 int norm_or_clip(int32_t n_tensors, const int64_t* numels, const void* const* ptrs, const int32_t* dtypes,
                  void* const* out, double max_norm, bool norm_given, float* norm, void* workspace,
                  int64_t workspace_bytes, void* stream) {
     int s = check_list(n_tensors, numels);
     if (s) return s;
-    if (ptrs == nullptr || dtypes == nullptr) return fail(DDP_E_ARG, "NULL pointer argument");
+    if ((s = check_dtypes(n_tensors, dtypes))) return s;
+    if (ptrs == nullptr) return fail(DDP_E_ARG, "ptrs is NULL");
     if ((s = check_norm_ptr(norm))) return s;
-    if (!norm_given && (s = check_workspace(workspace, workspace_bytes, DDP_NORM_WORKSPACE_BYTES))) return s;
+    const bool partials = !norm_given && !ddp::norm_is_small(n_tensors, numels, dtypes, out != nullptr);
+    if (partials && (s = check_workspace(workspace, workspace_bytes, DDP_NORM_WORKSPACE_BYTES))) return s;
     std::vector<Span> spans;
     spans.reserve((out != nullptr ? 2 : 1) * static_cast<size_t>(n_tensors) + 2);
     for (int32_t t = 0; t < n_tensors; ++t) {
-        if (!valid_dtype(dtypes[t])) return fail(DDP_E_ARG, "dtypes[%d] = %d is unknown", t, dtypes[t]);
         const int es = elem_bytes(dtypes[t]);
         if ((s = check_tensor(ptrs[t], numels[t], es, "ptrs", t))) return s;
         if (out != nullptr && (s = check_tensor(out[t], numels[t], es, "out", t))) return s;
@@ -1428,7 +1440,7 @@ int norm_or_clip(int32_t n_tensors, const int64_t* numels, const void* const* pt
         if (out != nullptr && !in_place) spans.push_back(span_of(out[t], numels[t] * es, true, "out", t));
     }
     spans.push_back(span_of(norm, sizeof(float), !norm_given, "norm", 0));
-    if (!norm_given) spans.push_back(span_of(workspace, DDP_NORM_WORKSPACE_BYTES, true, "workspace", 0));
+    if (partials) spans.push_back(span_of(workspace, DDP_NORM_WORKSPACE_BYTES, true, "workspace", 0));
     if ((s = check_written(spans))) return s;
 
     ddp::NormLaunch l{};
@@ -1437,18 +1449,13 @@ int norm_or_clip(int32_t n_tensors, const int64_t* numels, const void* const* pt
     l.in = ptrs;
     l.dtypes = dtypes;
     l.out = out;
-    l.partials = norm_given ? nullptr : static_cast<double*>(workspace);
+    l.norm_given = norm_given;
+    l.partials = partials ? static_cast<double*>(workspace) : nullptr;
     l.norm = norm;
     l.max_norm = static_cast<float>(max_norm);
     l.stream = stream;
     const char* msg = nullptr;
-    int partials = 0;
-    int e = norm_given ? 0 : ddp::launch_square_sums(l, &partials, &msg);
-    // The clipping kernel adds the partials itself; with no element at all
-    // there is no such launch.
-    if (e == 0 && !norm_given && (out == nullptr || partials == 0))
-        e = ddp::launch_norm_of(l.partials, partials, nullptr, norm, stream, &msg);
-    if (e == 0 && out != nullptr) e = ddp::launch_clip(l, partials, &msg);
+    const int e = out == nullptr ? ddp::launch_norm(l, &msg) : ddp::launch_clip(l, &msg);
     if (e != 0) return hip_fail(e, msg);
     return ok();
 }
@@ -1470,7 +1477,7 @@ int64_t norm_workgroups(const ddp::RingLaunch& l, int64_t bucket_elems) {
 }
 
 int64_t norm_workspace(int64_t workgroups) {
-    const int64_t fold = workgroups > ddp::kNormFoldOver ? ddp::kNormFold : 0;
+    const int64_t fold = workgroups > ddp::kNormFoldOver ? ddp::kNormFold + 1 : 0;
     return (workgroups + fold) * static_cast<int64_t>(sizeof(double));
 }
 
@@ -1516,6 +1523,7 @@ int ring_norm(ddp_reduce_op op, int32_t P, int32_t chunking, const void* const* 
     if (nspan.lo < wspan.hi && wspan.lo < nspan.hi) return fail(DDP_E_OVERLAP, "norm overlaps workspace");
 
     l.partials = static_cast<double*>(workspace);
+    if (groups > ddp::kNormFoldOver) l.zero = reinterpret_cast<uint64_t*>(l.partials + groups + ddp::kNormFold);
     int e = bucket_elems != 0 ? launch_buckets(l, bucket_elems, &msg) : ddp::launch_ring_reduce(l, &msg);
     if (e == 0) e = ddp::launch_norm_of(l.partials, groups, l.partials + groups, norm, stream, &msg);
     if (e != 0) return hip_fail(e, msg);
@@ -1600,6 +1608,16 @@ int grad_norm_multi(int32_t n_tensors, const int64_t* numels, const void* const*
         return norm_or_clip(n_tensors, numels, ptrs, dtypes, nullptr, 0.0, false, norm, workspace, workspace_bytes,
                             stream);
     });
+}
+
+int grad_norm_workspace_bytes(int32_t n_tensors, const int64_t* numels, const int32_t* dtypes, int32_t clip,
+                              int64_t* bytes) {
+    int s = check_list(n_tensors, numels);
+    if (s) return s;
+    if ((s = check_dtypes(n_tensors, dtypes))) return s;
+    if (bytes == nullptr) return fail(DDP_E_ARG, "bytes is NULL");
+    *bytes = ddp::norm_is_small(n_tensors, numels, dtypes, clip != 0) ? 0 : DDP_NORM_WORKSPACE_BYTES;
+    return ok();
 }
 
 int grad_clip_multi(int32_t n_tensors, const int64_t* numels, const void* const* ptrs, const int32_t* dtypes,

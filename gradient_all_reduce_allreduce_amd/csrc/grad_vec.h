@@ -51,6 +51,15 @@ __device__ __forceinline__ void store_elem(char* p, float x) {
     }
 }
 
+// A value that every lane reads and that no kernel running now writes, through
+// the constant address space: a scalar load.  Through a plain pointer the
+// compiler cannot rule out the kernel's own stores and takes a vector load,
+// which would wait behind the tile's data.
+template <class T>
+__device__ __forceinline__ T load_uniform(const T* p) {
+    return *(const __attribute__((address_space(4))) T*)(p);
+}
+
 // The clipping factor min(1, max_norm / (norm + 1e-6)) in float32, one
 // rounding per operation.  No limit (infinite max_norm) never scales; a
 // norm that is infinite gives 0 and one that is NaN gives NaN.
@@ -61,13 +70,36 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
     return c > 1.0f ? 1.0f : c;
 }
 
-// Sum of `x` over the workgroup's waves in a fixed order, in every lane.
+// x plus the value of another lane, chosen by a data-parallel-primitive
+// control; lanes it does not reach add zero.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_lane(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, true);
+    return x + __builtin_bit_cast(double, lo | static_cast<uint64_t>(hi) << 32);
+}
+
+// The sum over the wave's lanes in a fixed order, in lane 63: shifts by 1, 2,
+// 4 and 8 within each row of 16 lanes, then row sums into the next row and
+// the lower half's into the upper.  In registers, where exchanging lanes
+// through the LDS crossbar would wait a round trip for each of six steps.
+__device__ __forceinline__ double wave_sum63(double x) {
+    x = add_lane<0x111, 0xf>(x);
+    x = add_lane<0x112, 0xf>(x);
+    x = add_lane<0x114, 0xf>(x);
+    x = add_lane<0x118, 0xf>(x);
+    x = add_lane<0x142, 0xa>(x);
+    return add_lane<0x143, 0xc>(x);
+}
+
+// The sum over the workgroup in a fixed order, in every lane.  Once per
+// kernel: a second call would need a barrier before it.
 template <int BLOCK>
 __device__ __forceinline__ double block_sum(double x) {
     __shared__ double part[BLOCK / 64];
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    x = wave_sum63(x);
+    if ((threadIdx.x & 63) == 63) part[threadIdx.x >> 6] = x;
     __syncthreads();
     double s = part[0];
 #pragma unroll

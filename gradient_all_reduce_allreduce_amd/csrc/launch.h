@@ -151,9 +151,10 @@ struct RingLaunch {
     int64_t seg2;
     int seg2_chunking;
     // kAllReduce without sgd: where each workgroup leaves the sum of the
-    // squares it wrote (ring_workgroups of them), or null; and whether only
-    // rank 0 receives the result then.
+    // squares it wrote (ring_workgroups of them), or null; then also a word
+    // to clear on the way, and whether only rank 0 receives the result.
     double* partials;
+    uint64_t* zero;
     int one_copy;
 };
 

@@ -7,8 +7,24 @@
 
 namespace ddp {
 
-// Partial sums a norm leaves in its workspace at most, one per workgroup.
+// Longest tensor these calls accept: 2^36 elements, 256 GiB of float32, so
+// that a tensor's tiles are below 2^28 at the smallest tile.
+constexpr int64_t kMaxGradElems = int64_t(1) << 36;
+// Tiles of one launch, and its one-wave workgroups at most (a grid holds
+// fewer than 2^32 lanes; each workgroup walks on by the grid's size).
+constexpr int64_t kMaxTiles = int64_t(1) << 30;
+constexpr uint32_t kMaxWaveGrid = 1u << 25;
+
+// Partial sums a norm leaves in its workspace at most, one per workgroup:
+// 4 workgroups of 256 lanes per CU.
 constexpr int kNormPartials = DDP_NORM_WORKSPACE_BYTES / static_cast<int>(sizeof(double));
+// Up to so many tensors (with elements) of so many bytes together, one
+// workgroup takes the norm, and scales, in one launch.
+constexpr int kSmallTensors = 64;
+constexpr int64_t kSmallNormBytes = 512 << 10;
+constexpr int64_t kSmallClipBytes = 256 << 10;
+// One-wave workgroups of the scaling per CU.
+constexpr int kClipWgPerCu = 12;
 
 // The global norm of n_tensors gradient tensors, and their scaling.
 struct NormLaunch {
@@ -16,23 +32,32 @@ struct NormLaunch {
     const int64_t* numels;
     const void* const* in;
     const int32_t* dtypes;    // ddp_dtype of each tensor
-    void* const* out;         // clip: where the scaled tensors go
-    double* partials;         // [kNormPartials], device; null when the norm is given
-    float* norm;              // device: the norm, written (partials) or read
+    void* const* out;         // clip: where the scaled tensors go; else null
+    bool norm_given;
+    double* partials;         // [kNormPartials], device; null: small, or the norm is given
+    float* norm;              // device: the norm, written or (given) read
     float max_norm;
     void* stream;
 };
+// Whether these take the one-workgroup path, which needs no partials.
+bool norm_is_small(int32_t n_tensors, const int64_t* numels, const int32_t* dtypes, bool clip);
+int launch_norm(const NormLaunch& l, const char** msg);
+// out = in * min(1, max_norm / (norm + 1e-6)), the norm taken first unless
+// it is given.
+int launch_clip(const NormLaunch& l, const char** msg);
 
-// The squares' sums of every tensor into l.partials; *n_partials of them.
-int launch_square_sums(const NormLaunch& l, int* n_partials, const char** msg);
-// norm = sqrt(sum of count partials); more than kNormFoldOver of them are
-// first folded to kNormFold in `fold` (not read otherwise).
-constexpr int64_t kNormFoldOver = 16384;
-constexpr int kNormFold = 512;
+// norm = sqrt(sum of count partials).  More than kNormFoldOver of them are
+// summed by kNormFold workgroups through `fold` (not touched otherwise):
+// kNormFold sums and a count that is zero when this launch starts.  On
+// 99,832 partials (P = 8, 25.6M elements) 64 workgroups of 1,024 lanes add 3.7
+// us to the all-reduce, 256 of 256 lanes 7.7 us (each of them takes a turn
+// at the count) and one of 1,024 lanes 26 us; an empty launch adds 1.6 us.
+constexpr int64_t kNormFoldOver = 4096;
+constexpr int kNormFold = 64;
 int launch_norm_of(const double* partials, int64_t count, double* fold, float* norm, void* stream, const char** msg);
-// out = in * min(1, max_norm / (norm + 1e-6)); with partials (n_partials of
-// them) the norm is their root and is written to l.norm too.
-int launch_clip(const NormLaunch& l, int n_partials, const char** msg);
+
+// One-wave workgroups of the AdamW step per CU.
+constexpr int kAdamWWgPerCu = 12;
 
 // One AdamW step on n_tensors tensors.
 struct AdamWLaunch {

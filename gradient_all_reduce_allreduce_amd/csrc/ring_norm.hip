@@ -8,6 +8,7 @@
 // workgroup -- one wave, one tile -- adds its lanes in a fixed order and
 // writes one partial; a second, small launch adds the partials
 // (grad_norm.hip).
+#include "grad_vec.h"
 #include "ring_norm.h"
 
 namespace ddp {
@@ -20,11 +21,14 @@ __device__ __forceinline__ KRingNorm norm_args() {
     return (KRingNorm)(__builtin_amdgcn_kernarg_segment_ptr());
 }
 
-// The sum over the wave's lanes, in every lane.
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
-    return x;
+// Leaves the wave's sum.  The first workgroup of a call also clears the count
+// that the partials' sum starts from (grad_norm.hip).
+__device__ __forceinline__ void leave(KRingNorm a, double sq) {
+    sq = gv::wave_sum63(sq);
+    if (threadIdx.x == 63) {
+        a->partials[blockIdx.x] = sq;
+        if (blockIdx.x == 0 && a->zero != nullptr) *a->zero = 0;
+    }
 }
 
 template <int P, bool INB, bool OUTB>
@@ -32,8 +36,7 @@ __global__ __launch_bounds__(kBlock) void ring_norm_kernel(RingNormArgs) {
     const KRingNorm a = norm_args();
     double sq = 0.0;
     ring_reduce_body<P, INB, OUTB, false, true>(&sq, a->one_copy != 0);
-    sq = wave_sum(sq);
-    if (threadIdx.x == 0) a->partials[blockIdx.x] = sq;
+    leave(a, sq);
 }
 
 template <int P, bool INB, bool OUTB>
@@ -42,8 +45,7 @@ __global__ __launch_bounds__(kBlock) void ring_norm_scalar_kernel(RingNormArgs) 
     const uint32_t i = blockIdx.x * kBlock + threadIdx.x;
     double sq = 0.0;
     if (i < a->ring.n) process_element<P, INB, OUTB, false, true>(&a->ring, i, &sq, a->one_copy != 0);
-    sq = wave_sum(sq);
-    if (threadIdx.x == 0) a->partials[blockIdx.x] = sq;
+    leave(a, sq);
 }
 
 template <bool INB, bool OUTB, bool SCALAR>

@@ -78,6 +78,8 @@ int wg_per_cu(const RingLaunch& l) {
         case kAllGather: return wg_per_cu_for(DDP_KF_ALL_GATHER, kAgWgPerCu);
         case kTree: return wg_per_cu_for(DDP_KF_TREE, tree_wg_per_cu(l.P, ib, ob));
         default:
+            if (l.partials != nullptr)
+                return wg_per_cu_for(DDP_KF_RING, ring_norm_wg_per_cu(l.P, ib, ob, l.one_copy != 0));
             if (l.sgd) return wg_per_cu_for(DDP_KF_RING_SGD, sgd_wg_per_cu(l.P, ib, l.write_out != 0));
             return wg_per_cu_for(DDP_KF_RING, ring_wg_per_cu(l.P, ib, ob));
     }
@@ -198,6 +200,7 @@ int launch_ring_reduce(const RingLaunch& l, const char** msg) {
         if (l.partials != nullptr) {
             na.ring = a;
             na.partials = l.partials + partials;
+            na.zero = l.zero;
             na.one_copy = l.one_copy;
             partials += grid;
             args[0] = &na;

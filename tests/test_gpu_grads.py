@@ -451,7 +451,7 @@ def test_allreduce_norm_buckets(P, C, E, n, copies):
 
 
 def test_allreduce_norm_many_partials():
-    """Past 16,384 workgroups the sum has a second level."""
+    """Past 4,096 workgroups the sum has a second level."""
     P, n = 8, 256 * 17_000 + 100
     X = rank_draw(P, n, "bf16", seed=3)
     out, norm = ddp.allreduce_norm(to_device(X, "bf16"), "mean", P, out_dtype=torch.float32)

@@ -21,7 +21,7 @@ def at(k, off=0):
 
 
 def norm_args(**change):
-    a = dict(numels=[100, 0, 7], ptrs=[at(0), 0, at(2)], dtypes=[ddp.F32, ddp.BF16, ddp.BF16], workspace=WS,
+    a = dict(numels=[200_000, 0, 7], ptrs=[at(0), 0, at(2)], dtypes=[ddp.F32, ddp.BF16, ddp.BF16], workspace=WS,
              workspace_bytes=ddp.NORM_WORKSPACE_BYTES, norm=NORM)
     a.update(change)
     return a
@@ -57,8 +57,9 @@ def refused(fn, args, status, text=None):
 
 
 LISTS = [
-    (dict(numels=[100, -1, 7]), N.DDP_E_ARG, "negative"),
+    (dict(numels=[200_000, -1, 7]), N.DDP_E_ARG, "negative"),
     (dict(numels=[(1 << 40) + 1, 0, 7]), N.DDP_E_ARG, "2^40"),
+    (dict(numels=[(1 << 36) + 1, 0, 7]), N.DDP_E_UNSUPPORTED, "2^36"),
     (dict(numels=[], ptrs=[], dtypes=[]), N.DDP_E_ARG, "n_tensors"),
     (dict(ptrs=[0, 0, at(2)]), N.DDP_E_ARG, "NULL"),
     (dict(ptrs=[at(0, 2), 0, at(2)]), N.DDP_E_ALIGN, "ptrs[0]"),
@@ -87,7 +88,7 @@ def test_norm_refusals(change, status, text):
     (dict(out=[at(4, 2), 0, at(6)]), N.DDP_E_ALIGN, "out[0]"),
     (dict(out=[at(0, 4), 0, at(6)]), N.DDP_E_OVERLAP, None),        # over its own input, not in place
     (dict(out=[at(2), 0, at(6)]), N.DDP_E_OVERLAP, None),           # another tensor's input
-    (dict(out=[at(4), 0, at(4, 398)]), N.DDP_E_OVERLAP, None),      # two outputs, by one element
+    (dict(out=[at(4), 0, at(4, 799_998)]), N.DDP_E_OVERLAP, None),      # two outputs, by one element
     # the same tensor twice, in place
     (dict(numels=[9, 9, 0], ptrs=[at(0), at(0), 0], dtypes=[ddp.F32] * 3, out=[at(0), at(0), 0]),
      N.DDP_E_OVERLAP, None),
@@ -163,14 +164,29 @@ def test_workspace_bytes_grow_with_the_workgroups():
     # chunks are shorter than a tile
     assert f(8, 8, ddp.F32, ddp.F32, 256 * 1000) == 8000
     assert f(8, 8, ddp.F32, ddp.F32, 640) == 80
-    # past 16,384 workgroups the sum has a second level of 512
-    assert f(8, 8, ddp.F32, ddp.F32, 256 * 20000) == 8 * (20000 + 512)
+    # past 4,096 workgroups the sum has a second level: 64 sums and a count
+    assert f(8, 8, ddp.F32, ddp.F32, 256 * 20000) == 8 * (20000 + 65)
     # buckets that are one ring need no more than the flat buffer
     assert f(8, 8, ddp.F32, ddp.F32, 4 * 8192, 8192) == f(8, 8, ddp.F32, ddp.F32, 4 * 8192)
     with pytest.raises(DdpError):
         f(8, 0, ddp.F32, ddp.F32, 10)
     with pytest.raises(DdpError):
         f(8, 8, ddp.F32, ddp.F32, 10, 3)
+
+
+def test_norm_workspace_bytes():
+    f = ddp.grad_norm_workspace_bytes
+    kb = 256                                              # float32 elements per KiB
+    assert f([512 * kb], [ddp.F32]) == 0 and f([1024 * kb], [ddp.BF16]) == 0
+    assert f([512 * kb, 1], [ddp.F32] * 2) == ddp.NORM_WORKSPACE_BYTES
+    assert f([256 * kb], [ddp.F32], True) == 0
+    assert f([256 * kb + 1], [ddp.F32], True) == ddp.NORM_WORKSPACE_BYTES
+    assert f([1] * 64 + [0], [ddp.F32] * 65) == 0
+    assert f([1] * 65, [ddp.F32] * 65) == ddp.NORM_WORKSPACE_BYTES
+    with pytest.raises(DdpError):
+        f([-1], [ddp.F32])
+    with pytest.raises(DdpError):
+        f([1], [3])
 
 
 def test_python_refusals():
