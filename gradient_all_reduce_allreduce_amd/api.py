@@ -27,6 +27,7 @@ Tensor-level helpers:
 """
 
 import ctypes
+import functools
 
 import numpy as np
 
@@ -329,13 +330,13 @@ def grad_norm_multi(numels, ptrs, dtypes, workspace, workspace_bytes, norm, stre
                                    workspace, workspace_bytes, norm, stream))
 
 
-def grad_norm_workspace_bytes(numels, dtypes, clip=False):
-    """Workspace of grad_norm_multi, or grad_clip_multi (host only)."""
-    if len(numels) != len(dtypes):
-        raise ValueError("numels and dtypes must have one entry per tensor")
+def grad_norm_workspace_bytes(numels, ptrs, dtypes):
+    """Workspace of grad_norm_multi and grad_clip_multi (host only)."""
+    if not len(numels) == len(ptrs) == len(dtypes):
+        raise ValueError("numels, ptrs and dtypes must have one entry per tensor")
     b = ctypes.c_int64(0)
-    _check(N.lib().grad_norm_workspace_bytes(len(numels), _long_array(numels), _int_array(dtypes), int(bool(clip)),
-                                             ctypes.byref(b)))
+    _check(N.lib().grad_norm_workspace_bytes(len(numels), _long_array(numels), N.pointer_array(ptrs),
+                                             _int_array(dtypes), ctypes.byref(b)))
     return b.value
 
 
@@ -404,13 +405,17 @@ KERNEL_FAMILIES = dict(N.KERNEL_FAMILIES)
 
 # --------------------------------------------------------- torch level ----
 
+_DTYPE_CODES = {}
+
+
 def torch_dtype_code(dtype):
-    import torch
-    if dtype == torch.float32:
-        return F32
-    if dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported element type {dtype}")
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float32: F32, torch.bfloat16: BF16})
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported element type {dtype}")
+    return code
 
 
 def current_stream(device):
@@ -441,10 +446,12 @@ def _rank_tensors(tensors, what):
     if not 1 <= len(tensors) <= MAX_RANKS:
         raise ValueError(f"{what}: need 1..{MAX_RANKS} rank tensors, got {len(tensors)}")
     t0 = tensors[0]
+    device, dtype, numel = t0.get_device(), t0.dtype, t0.numel()
     for t in tensors:
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError(f"{what}: tensors must live on the GPU")
-        if t.device != t0.device or t.dtype != t0.dtype or t.numel() != t0.numel():
+        if d != device or t.dtype != dtype or t.numel() != numel:
             raise ValueError(f"{what}: every rank needs the same device, dtype and size")
         if not t.is_contiguous():
             raise ValueError(f"{what}: tensors must be contiguous")
@@ -802,15 +809,10 @@ def allreduce_sgd(grads, w, v, lr, mu, op="mean", chunking=None, out=None, bucke
 
 # ------------------------------------------- norm, clipping, AdamW --------
 
-def _on_device(index, call):
-    """``call(stream)`` with GPU ``index`` current (a launch on its default
-    stream, which names no device, must find it so) and the handle of that
-    GPU's current stream."""
+def _raw_stream(index):
+    """Handle of GPU ``index``'s current stream."""
     import torch
-    if torch.cuda.current_device() == index:
-        return call(torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(index):
-        return call(torch._C._cuda_getCurrentRawStream(index))
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _tensor_list(tensors, what, dtypes):
@@ -853,12 +855,13 @@ class MultiGrad:
         import torch
         self.grads = _tensor_list(grads, "MultiGrad", (torch.float32, torch.bfloat16))
         self.device = self.grads[0].device
+        self._index = self.device.index
+        self._new_norm = functools.partial(torch.empty_like, torch.empty((), dtype=torch.float32, device=self.device))
         numels = [g.numel() for g in self.grads]
         codes = [torch_dtype_code(g.dtype) for g in self.grads]
-        self._list = (len(numels), _long_array(numels), N.pointer_array([g.data_ptr() for g in self.grads]),
-                      _int_array(codes))
-        self._norm_bytes = grad_norm_workspace_bytes(numels, codes)
-        self._clip_bytes = grad_norm_workspace_bytes(numels, codes, True)
+        ptrs = [g.data_ptr() for g in self.grads]
+        self._list = (len(numels), _long_array(numels), N.pointer_array(ptrs), _int_array(codes))
+        self._bytes = grad_norm_workspace_bytes(numels, ptrs, codes)
 
     def _match(self, tensors, what, dtypes):
         """Tensors of the gradients' sizes, one each, on their device."""
@@ -871,14 +874,20 @@ class MultiGrad:
     def norm(self):
         """The global 2-norm of all gradients, a float32 scalar tensor."""
         import torch
+        # With another GPU current, a launch on the default stream, whose
+        # handle names no GPU, would go there.
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.norm()
+        norm = self._new_norm()
+        ws = self._workspace()
+        _check(N.lib().grad_norm_multi(*self._list, ws.data_ptr() if ws is not None else None, self._bytes,
+                                       norm.data_ptr(), _raw_stream(self._index)))
+        return norm
 
-        def call(stream):
-            norm = torch.empty((), dtype=torch.float32, device=self.device)
-            ws = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device) if self._norm_bytes else None
-            _check(N.lib().grad_norm_multi(*self._list, ws.data_ptr() if ws is not None else None, self._norm_bytes,
-                                           norm.data_ptr(), stream))
-            return norm
-        return _on_device(self.device.index, call)
+    def _workspace(self):
+        import torch
+        return torch.empty(self._bytes, dtype=torch.uint8, device=self.device) if self._bytes else None
 
     def bind_clip(self, out=None):
         """Returns ``run(max_norm, norm=None)``, which scales every gradient
@@ -895,18 +904,19 @@ class MultiGrad:
                 raise ValueError("clip out: every output must have its gradient's type")
 
         def run(max_norm, norm=None):
-            def call(stream):
-                result, ws = norm, None
-                if norm is None:
-                    result = torch.empty((), dtype=torch.float32, device=self.device)
-                    if self._clip_bytes:
-                        ws = torch.empty(self._clip_bytes, dtype=torch.uint8, device=self.device)
-                _check(N.lib().grad_clip_multi(*self._list, optrs, max_norm, norm is not None, result.data_ptr(),
-                                               ws.data_ptr() if ws is not None else None, self._clip_bytes, stream))
-                return result
-            if norm is not None:
+            if torch.cuda.current_device() != self._index:
+                with torch.cuda.device(self._index):
+                    return run(max_norm, norm)
+            given, ws = norm is not None, None
+            if given:
                 _scalar(norm, torch.float32, self.device, "norm")
-            return _on_device(self.device.index, call)
+            else:
+                norm = self._new_norm()
+                ws = self._workspace()
+            _check(N.lib().grad_clip_multi(*self._list, optrs, max_norm, given, norm.data_ptr(),
+                                           ws.data_ptr() if ws is not None else None, self._bytes,
+                                           _raw_stream(self._index)))
+            return norm
 
         run.tensors = (self.grads, out)
         return run
@@ -940,15 +950,17 @@ class MultiGrad:
         def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
             if (norm is None) != (max_norm is None):
                 raise ValueError("adamw: norm and max_norm come together")
-            step_dev = None
+            if torch.cuda.current_device() != self._index:
+                with torch.cuda.device(self._index):
+                    return run(lr, step, betas, eps, weight_decay, norm, max_norm)
+            step_dev = norm_dev = None
             if isinstance(step, torch.Tensor):
-                step_dev = _scalar(step, torch.int64, self.device, "step").data_ptr()
-                step = 0
+                step_dev, step = _scalar(step, torch.int64, self.device, "step").data_ptr(), 0
             if norm is not None:
-                norm = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
-            _on_device(self.device.index, lambda stream: _check(N.lib().adamw_step_multi(
-                count, numels, ptrs, gcode, wptrs, mptrs, vptrs, pptrs, pcode, lr, betas[0], betas[1], eps,
-                weight_decay, step, step_dev, norm, max_norm if norm is not None else 0.0, stream)))
+                norm_dev = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
+            _check(N.lib().adamw_step_multi(count, numels, ptrs, gcode, wptrs, mptrs, vptrs, pptrs, pcode, lr,
+                                            betas[0], betas[1], eps, weight_decay, step, step_dev, norm_dev,
+                                            max_norm or 0.0, _raw_stream(self._index)))
 
         run.tensors = (self.grads, w, m, v, params)
         return run
@@ -973,6 +985,11 @@ def adamw_step(grads, w, m, v, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_de
     MultiGrad(grads).bind_adamw(w, m, v, params)(lr, step, betas, eps, weight_decay, norm, max_norm)
 
 
+# The workspace depends on the sizes alone; a training loop asks for the same
+# ones at every step.
+_norm_workspace = functools.lru_cache(maxsize=256)(allreduce_norm_workspace_bytes)
+
+
 def allreduce_norm(tensors, op="sum", chunking=None, out=None, out_dtype=None, bucket_elems=None):
     """``allreduce`` that also leaves the global 2-norm of the result as one
     rank holds it; returns (outputs, norm), the norm a float32 scalar tensor.
@@ -995,16 +1012,16 @@ def allreduce_norm(tensors, op="sum", chunking=None, out=None, out_dtype=None, b
     C = chunking or P
     if bucket_elems is not None and bucket_elems < 1:
         raise ValueError("allreduce_norm: bucket_elems must be at least 1")
-    need = allreduce_norm_workspace_bytes(P, C, icode, ocode, n, bucket_elems or 0)
+    need = _norm_workspace(P, C, icode, ocode, n, bucket_elems or 0)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return allreduce_norm(tensors, op, chunking, out, out_dtype, bucket_elems)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    norm = torch.empty((), dtype=torch.float32, device=device)
     ins, outs = [t.data_ptr() for t in tensors], [t.data_ptr() for t in out]
-
-    def call(stream):
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        end = (norm.data_ptr(), ws.data_ptr(), need, stream)
-        if bucket_elems is not None:
-            allreduce_ring_norm_buckets(op, P, C, ins, icode, outs, ocode, n, bucket_elems, *end)
-        else:
-            allreduce_ring_norm(op, P, C, ins, icode, outs, ocode, n, *end)
-        return out, norm
-    return _on_device(device.index, call)
+    end = (norm.data_ptr(), ws.data_ptr(), need, _raw_stream(device.index))
+    if bucket_elems is not None:
+        allreduce_ring_norm_buckets(op, P, C, ins, icode, outs, ocode, n, bucket_elems, *end)
+    else:
+        allreduce_ring_norm(op, P, C, ins, icode, outs, ocode, n, *end)
+    return out, norm

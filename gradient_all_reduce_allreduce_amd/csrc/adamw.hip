@@ -40,9 +40,9 @@ using rr::u32x4;
 constexpr int kBlock = 64;                             // one wave
 constexpr uint32_t kTileElems = kBlock * 4;
 constexpr uint32_t kLineElems = 32;                    // float32 per 128-byte line
-// Tensors per launch: as many as the arguments hold, or few, whose arguments
-// are quicker to hand over.
-constexpr int kManyTensors = 144;
+// Tensors (or pieces of them) per launch: as many as the arguments hold, or
+// few, whose arguments are quicker to hand over.
+constexpr int kManyTensors = 162;
 constexpr int kFewTensors = 16;
 
 template <int CAP>
@@ -53,10 +53,10 @@ struct AdamWArgs {
     char* m[CAP];
     char* v[CAP];
     char* p[CAP];
-    uint64_t numel[CAP];
+    uint32_t count[CAP];     // elements, up to kMaxPiece
     uint32_t first_tile[CAP];
     int32_t n;
-    uint32_t tiles;          // of all tensors
+    uint32_t tiles;          // of all pieces
     const float* norm;
     const int64_t* step;     // device; null: step_size and root2 hold the step's
     double b1, b2, lr;       // with `step`
@@ -68,7 +68,7 @@ struct AdamWArgs {
     float step_size;
     float root2;
 };
-static_assert(sizeof(AdamWArgs<kManyTensors>) <= 7800, "kernel arguments must stay under the 8,000 bytes measured to pass");
+static_assert(sizeof(AdamWArgs<kManyTensors>) <= kArgBytes, "kernel arguments");
 template <int CAP>
 using KAdamW = const __attribute__((address_space(4))) AdamWArgs<CAP>*;
 
@@ -142,8 +142,6 @@ __device__ __forceinline__ bool factors(KAdamW<CAP> a, float norm, int64_t t, Fa
 template <int CAP, bool GB, int PM>
 __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs<CAP>) {
     const KAdamW<CAP> a = (KAdamW<CAP>)(__builtin_amdgcn_kernarg_segment_ptr());
-    constexpr uint32_t GES = GB ? 2 : 4;
-    constexpr uint32_t PES = PM == 2 ? 2 : 4;
     const uint32_t tiles = a->tiles;
     const float norm = a->norm != nullptr ? gv::load_uniform(a->norm) : 0.0f;
     const int64_t step = a->step != nullptr ? gv::load_uniform(a->step) : 1;
@@ -158,59 +156,57 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs<CAP>) {
         char* const m = a->m[t];
         char* const v = a->v[t];
         char* const p = a->p[t];
-        const int64_t n = static_cast<int64_t>(a->numel[t]);
-        const int64_t lead = static_cast<int64_t>((reinterpret_cast<uint64_t>(w) >> 2) % kLineElems);
-        const int64_t at = static_cast<int64_t>(tile - a->first_tile[t]) * kTileElems - lead;
-        Factors f;
-        if (at >= 0 && at + kTileElems <= n) {
-            const int64_t i = at + threadIdx.x * 4;
-            u32x4 gq;
+        const int32_t n = static_cast<int32_t>(a->count[t]);
+        const int32_t lead = static_cast<int32_t>((reinterpret_cast<uint64_t>(w) >> 2) % kLineElems);
+        const int32_t at = static_cast<int32_t>((tile - a->first_tile[t]) * kTileElems) - lead;
+        const int64_t i = at + static_cast<int32_t>(threadIdx.x * 4);
+        const bool whole = (at >= 0 && at + static_cast<int32_t>(kTileElems) <= n) || (i >= 0 && i + 4 <= n);
+        u32x4 gq, wq, mq, vq;
+        if (whole) {
             if constexpr (GB) {
                 const u32x2 h = gv::load2_nt(g + i * 2);
                 gq = u32x4{h[0], h[1], 0u, 0u};
             } else {
                 gq = gv::load4_nt(g + i * 4);
             }
-            u32x4 wq = gv::load4_nt(w + i * 4);
-            u32x4 mq = gv::load4_nt(m + i * 4);
-            u32x4 vq = gv::load4_nt(v + i * 4);
-            // The factors (divisions, two powers) while the tile's data is in
-            // flight.
-            if (!factors(a, norm, step, f)) return;
-            float wn[4];
+            wq = gv::load4_nt(w + i * 4);
+            mq = gv::load4_nt(m + i * 4);
+            vq = gv::load4_nt(v + i * 4);
+        } else {   // over a tensor's ends
+            gq = gv::load_some<GB, 4>(g, i, n);
+            wq = gv::load_some<false, 4>(w, i, n);
+            mq = gv::load_some<false, 4>(m, i, n);
+            vq = gv::load_some<false, 4>(v, i, n);
+        }
+        // The factors (divisions, two powers) while the tile's data is in
+        // flight.
+        Factors f;
+        if (!factors(a, norm, step, f)) return;
+        float wn[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float me = __uint_as_float(mq[e]);
-                float ve = __uint_as_float(vq[e]);
-                wn[e] = __uint_as_float(wq[e]);
-                adamw_element(rr::elem<GB>(gq, e), wn[e], me, ve, f);
-                wq[e] = __float_as_uint(wn[e]);
-                mq[e] = __float_as_uint(me);
-                vq[e] = __float_as_uint(ve);
-            }
+        for (int e = 0; e < 4; ++e) {
+            float me = __uint_as_float(mq[e]);
+            float ve = __uint_as_float(vq[e]);
+            wn[e] = __uint_as_float(wq[e]);
+            adamw_element(rr::elem<GB>(gq, e), wn[e], me, ve, f);
+            wq[e] = __float_as_uint(wn[e]);
+            mq[e] = __float_as_uint(me);
+            vq[e] = __float_as_uint(ve);
+        }
+        const u32x2 h = {rr::bf16_bits(wn[0]) | (rr::bf16_bits(wn[1]) << 16),
+                         rr::bf16_bits(wn[2]) | (rr::bf16_bits(wn[3]) << 16)};
+        if (whole) {
             gv::store4_nt(w + i * 4, wq);
             gv::store4_nt(m + i * 4, mq);
             gv::store4_nt(v + i * 4, vq);
             if constexpr (PM == 1) gv::store4_nt(p + i * 4, wq);
-            if constexpr (PM == 2)
-                gv::store2_nt(p + i * 2, u32x2{rr::bf16_bits(wn[0]) | (rr::bf16_bits(wn[1]) << 16),
-                                               rr::bf16_bits(wn[2]) | (rr::bf16_bits(wn[3]) << 16)});
-            continue;
-        }
-        // A tensor's first or last tile: one element per lane.
-        if (!factors(a, norm, step, f)) return;
-        const int64_t lo = at < 0 ? 0 : at;
-        const int64_t hi = at + kTileElems < n ? at + kTileElems : n;
-        for (int64_t i = lo + threadIdx.x; i < hi; i += kBlock) {
-            float* const we = reinterpret_cast<float*>(w) + i;
-            float* const me = reinterpret_cast<float*>(m) + i;
-            float* const ve = reinterpret_cast<float*>(v) + i;
-            float x = *we, y = *me, z = *ve;
-            adamw_element(gv::load_elem<GB>(g + i * GES), x, y, z, f);
-            *we = x;
-            *me = y;
-            *ve = z;
-            if constexpr (PM != 0) gv::store_elem<PM == 2>(p + i * PES, x);
+            if constexpr (PM == 2) gv::store2_nt(p + i * 2, h);
+        } else {
+            gv::store_some<false, 4>(w, i, n, wq);
+            gv::store_some<false, 4>(m, i, n, mq);
+            gv::store_some<false, 4>(v, i, n, vq);
+            if constexpr (PM == 1) gv::store_some<false, 4>(p, i, n, wq);
+            if constexpr (PM == 2) gv::store_some<true, 4>(p, i, n, u32x4{h[0], h[1], 0u, 0u});
         }
     }
 }
@@ -251,24 +247,30 @@ int launch_all(const AdamWLaunch& l, const char** msg) {
         a.root2 = s.root2;
     }
     const void* fn = kernel_for<CAP>(l);
+    int64_t at = 0;   // element of tensor t that the next piece starts at
     for (int32_t t = 0; t < l.n_tensors;) {
         int64_t tiles = 0;
-        a.n = 0;
-        for (; t < l.n_tensors && a.n < CAP; ++t) {
-            const int64_t n = l.numels[t];
-            if (n == 0) continue;
-            const int64_t lead = static_cast<int64_t>((reinterpret_cast<uintptr_t>(l.w[t]) >> 2) % kLineElems);
-            const int64_t need = (lead + n + kTileElems - 1) / kTileElems;
-            if (tiles + need > kMaxTiles) break;
-            a.g[a.n] = static_cast<const char*>(l.grads[t]);
-            a.w[a.n] = reinterpret_cast<char*>(l.w[t]);
-            a.m[a.n] = reinterpret_cast<char*>(l.m[t]);
-            a.v[a.n] = reinterpret_cast<char*>(l.v[t]);
-            a.p[a.n] = l.params != nullptr ? static_cast<char*>(l.params[t]) : nullptr;
-            a.numel[a.n] = static_cast<uint64_t>(n);
-            a.first_tile[a.n] = static_cast<uint32_t>(tiles);
-            tiles += need;
-            ++a.n;
+        for (a.n = 0; t < l.n_tensors && a.n < CAP;) {
+            const int64_t count = std::min(l.numels[t] - at, kMaxPiece);
+            if (count > 0) {
+                const int64_t ges = l.grad_bf16 ? 2 : 4;
+                const int64_t pes = l.param_bf16 ? 2 : 4;
+                a.g[a.n] = static_cast<const char*>(l.grads[t]) + at * ges;
+                a.w[a.n] = reinterpret_cast<char*>(l.w[t] + at);
+                a.m[a.n] = reinterpret_cast<char*>(l.m[t] + at);
+                a.v[a.n] = reinterpret_cast<char*>(l.v[t] + at);
+                a.p[a.n] = l.params != nullptr ? static_cast<char*>(l.params[t]) + at * pes : nullptr;
+                a.count[a.n] = static_cast<uint32_t>(count);
+                a.first_tile[a.n] = static_cast<uint32_t>(tiles);
+                const int64_t lead = static_cast<int64_t>((reinterpret_cast<uintptr_t>(a.w[a.n]) >> 2) % kLineElems);
+                tiles += (lead + count + kTileElems - 1) / kTileElems;
+                at += count;
+                ++a.n;
+            }
+            if (at >= l.numels[t]) {
+                ++t;
+                at = 0;
+            }
         }
         if (a.n == 0) continue;
         a.tiles = static_cast<uint32_t>(tiles);

@@ -1367,12 +1367,8 @@ int guarded(F body) {
 int check_list(int32_t n_tensors, const int64_t* numels) {
     if (n_tensors < 1) return fail(DDP_E_ARG, "n_tensors = %d, must be >= 1", n_tensors);
     if (numels == nullptr) return fail(DDP_E_ARG, "numels is NULL");
-    for (int32_t t = 0; t < n_tensors; ++t) {
+    for (int32_t t = 0; t < n_tensors; ++t)
         if (const int s = check_length(numels[t], "numels[t]")) return s;
-        if (numels[t] > ddp::kMaxGradElems)
-            return fail(DDP_E_UNSUPPORTED, "numels[%d] = %lld is over 2^36 elements", t,
-                        static_cast<long long>(numels[t]));
-    }
     return DDP_OK;
 }
 
@@ -1426,7 +1422,7 @@ int norm_or_clip(int32_t n_tensors, const int64_t* numels, const void* const* pt
     if ((s = check_dtypes(n_tensors, dtypes))) return s;
     if (ptrs == nullptr) return fail(DDP_E_ARG, "ptrs is NULL");
     if ((s = check_norm_ptr(norm))) return s;
-    const bool partials = !norm_given && !ddp::norm_is_small(n_tensors, numels, dtypes, out != nullptr);
+    const bool partials = !norm_given && !ddp::norm_is_small(n_tensors, numels, ptrs, dtypes);
     if (partials && (s = check_workspace(workspace, workspace_bytes, DDP_NORM_WORKSPACE_BYTES))) return s;
     std::vector<Span> spans;
     spans.reserve((out != nullptr ? 2 : 1) * static_cast<size_t>(n_tensors) + 2);
@@ -1610,13 +1606,13 @@ int grad_norm_multi(int32_t n_tensors, const int64_t* numels, const void* const*
     });
 }
 
-int grad_norm_workspace_bytes(int32_t n_tensors, const int64_t* numels, const int32_t* dtypes, int32_t clip,
-                              int64_t* bytes) {
+int grad_norm_workspace_bytes(int32_t n_tensors, const int64_t* numels, const void* const* ptrs,
+                              const int32_t* dtypes, int64_t* bytes) {
     int s = check_list(n_tensors, numels);
     if (s) return s;
     if ((s = check_dtypes(n_tensors, dtypes))) return s;
-    if (bytes == nullptr) return fail(DDP_E_ARG, "bytes is NULL");
-    *bytes = ddp::norm_is_small(n_tensors, numels, dtypes, clip != 0) ? 0 : DDP_NORM_WORKSPACE_BYTES;
+    if (ptrs == nullptr || bytes == nullptr) return fail(DDP_E_ARG, "NULL pointer argument");
+    *bytes = ddp::norm_is_small(n_tensors, numels, ptrs, dtypes) ? 0 : DDP_NORM_WORKSPACE_BYTES;
     return ok();
 }
 

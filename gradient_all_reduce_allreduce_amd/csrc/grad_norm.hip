@@ -43,34 +43,36 @@ constexpr uint32_t tile_bytes(int block) { return static_cast<uint32_t>(block) *
 constexpr int kNormBlock = 256;
 // The scaling: one-wave workgroups, 4 KiB tiles, one each.
 constexpr int kClipBlock = 64;
-// Both for few small tensors: one workgroup whose waves take 4 KiB tiles.
+// Both for few small tensors: one workgroup whose waves hold up to four 4 KiB
+// tiles each.
 constexpr int kSmallBlock = 1024;
+constexpr int kSmallWaves = kSmallBlock / 64;
+constexpr int kSmallPerWave = kSmallTiles / kSmallWaves;
 // The partials' sum.
 constexpr int kSumBlock = 1024;
 
-// The tensors of one launch.  numel's top bit says bf16.
+// The pieces of one launch: a tensor, or up to kMaxPiece elements of one.
+// count's top bit says bf16.
 template <int CAP, bool OUT>
 struct SetArgs {
     static constexpr int kCap = CAP;
     static constexpr bool kOut = OUT;
     const char* in[CAP];
     char* out[OUT ? CAP : 1];
-    uint64_t numel[CAP];
+    uint32_t count[CAP];
     uint32_t first_tile[CAP];
-    int32_t n;                      // tensors, 1 .. CAP
-    uint32_t tiles;                 // of all tensors
+    int32_t n;                      // pieces, 1 .. CAP
+    uint32_t tiles;                 // of all pieces
     int32_t add;                    // norm: add to the partials already there
     int32_t in_place;               // clip: every output is its input
     double* partials;
     float* norm;
     float max_norm;
 };
-constexpr uint64_t kBf16Bit = uint64_t(1) << 63;
-typedef SetArgs<380, false> NormArgs;
-typedef SetArgs<272, true> ClipArgs;
-typedef SetArgs<kSmallTensors, true> SmallArgs;
-static_assert(sizeof(NormArgs) <= 7800 && sizeof(ClipArgs) <= 7800,
-              "kernel arguments must stay under the 8,000 bytes measured to pass");
+constexpr uint32_t kBf16Bit = 1u << 31;
+typedef SetArgs<490, false> NormArgs;
+typedef SetArgs<326, true> ClipArgs;
+static_assert(sizeof(NormArgs) <= kArgBytes && sizeof(ClipArgs) <= kArgBytes, "kernel arguments");
 
 template <class A>
 using Konst = const __attribute__((address_space(4))) A*;
@@ -79,30 +81,31 @@ __device__ __forceinline__ Konst<A> args() {
     return (Konst<A>)(__builtin_amdgcn_kernarg_segment_ptr());
 }
 
-// The tensor a tile lies in.  All uniform.
+// The piece a tile lies in, and where.  All uniform.  Elements count from the
+// piece's start; the tile's first one, on a line, may lie before it.
 struct Piece {
-    const char* base;   // the tensor's start, down to a line
-    uint64_t lo, hi;    // its bytes [lo, hi) from there
-    uint64_t at;        // the tile's first byte from there
+    const char* in;
+    int32_t n;
+    int32_t at;
     bool bf16;
 };
 template <class A>
 __device__ __forceinline__ Piece piece_of(Konst<A> a, int t, uint32_t tile, uint32_t bytes) {
     Piece p;
-    const uint64_t in = reinterpret_cast<uint64_t>(a->in[t]);
-    const uint64_t n = a->numel[t];
-    p.bf16 = (n & kBf16Bit) != 0;
-    p.lo = in % kLine;
-    p.base = reinterpret_cast<const char*>(in - p.lo);
-    p.hi = p.lo + (n & ~kBf16Bit) * (p.bf16 ? 2 : 4);
-    p.at = static_cast<uint64_t>(tile - a->first_tile[t]) * bytes;
+    p.in = a->in[t];
+    const uint32_t count = a->count[t];
+    p.bf16 = (count & kBf16Bit) != 0;
+    p.n = static_cast<int32_t>(count & ~kBf16Bit);
+    const uint32_t es = p.bf16 ? 1 : 2;   // shift
+    p.at = static_cast<int32_t>((tile - a->first_tile[t]) * (bytes >> es)) -
+           static_cast<int32_t>((reinterpret_cast<uint64_t>(p.in) % kLine) >> es);
     return p;
 }
 
-// The tensor holding a tile: the last whose first tile is not past it.  For a
+// The piece holding a tile: the last whose first tile is not past it.  For a
 // workgroup that looks up one tile: a binary search with scalar loads.
 template <class A>
-__device__ __forceinline__ int tensor_at(Konst<A> a, uint32_t tile) {
+__device__ __forceinline__ int piece_at(Konst<A> a, uint32_t tile) {
     int lo = 0;
     for (int hi = a->n - 1; lo < hi;) {
         const int mid = (lo + hi + 1) >> 1;
@@ -112,7 +115,7 @@ __device__ __forceinline__ int tensor_at(Konst<A> a, uint32_t tile) {
 }
 
 // For one that walks over many: every lane keeps some of the first tiles,
-// and the tensor is the count of those not past the tile (a few compares and
+// and the piece is the count of those not past the tile (a few compares and
 // bit counts, no memory).
 template <class A>
 struct Finder {
@@ -138,28 +141,49 @@ __device__ __forceinline__ void add_squares(const u32x4& x, double (&acc)[2]) {
     for (int e = 0; e < (BF16 ? 8 : 4); ++e) acc[e & 1] = square_to(acc[e & 1], rr::elem<BF16>(x, e));
 }
 
-// The squares of a tile, by BLOCK lanes of which this is `lane`.
+// Whether a tile of BLOCK lanes lies inside its piece.
 template <int BLOCK, bool BF16>
-__device__ __forceinline__ void tile_squares(const Piece& p, uint32_t lane, double (&acc)[2]) {
-    constexpr uint32_t ES = BF16 ? 2 : 4;
-    if (p.at >= p.lo && p.at + tile_bytes(BLOCK) <= p.hi) {
-        u32x4 x[kVecPerLane];
+__device__ __forceinline__ bool inside(const Piece& p) {
+    return p.at >= 0 && p.at + static_cast<int32_t>(tile_bytes(BLOCK) / (BF16 ? 2 : 4)) <= p.n;
+}
+
+// The element of the piece at which vector u of a lane of the tile starts.
+template <int BLOCK, bool BF16>
+__device__ __forceinline__ int32_t vector_at(const Piece& p, uint32_t u, uint32_t lane) {
+    return p.at + static_cast<int32_t>((u * BLOCK + lane) * (BF16 ? 8u : 4u));
+}
+
+// A lane's vectors of a tile; in a piece's first and last tile zeros in the
+// places past its ends, where single elements are read after all whole
+// vectors are on their way.
+template <int BLOCK, bool BF16>
+__device__ __forceinline__ void load_tile(const Piece& p, uint32_t lane, u32x4 (&x)[kVecPerLane]) {
+    constexpr int VE = BF16 ? 8 : 4;
+    constexpr int64_t ES = BF16 ? 2 : 4;
+    if (inside<BLOCK, BF16>(p)) {
 #pragma unroll
-        for (uint32_t u = 0; u < kVecPerLane; ++u) x[u] = gv::load4_nt(p.base + p.at + (u * BLOCK + lane) * 16u);
-#pragma unroll
-        for (uint32_t u = 0; u < kVecPerLane; ++u) add_squares<BF16>(x[u], acc);
+        for (uint32_t u = 0; u < kVecPerLane; ++u) x[u] = gv::load4_nt(p.in + static_cast<int64_t>(vector_at<BLOCK, BF16>(p, u, lane)) * ES);
         return;
     }
-    // A tensor's first or last tile: whole vectors where they fit.
+#pragma unroll
     for (uint32_t u = 0; u < kVecPerLane; ++u) {
-        const uint64_t o = p.at + (u * BLOCK + lane) * 16u;
-        if (o >= p.lo && o + 16 <= p.hi) {
-            add_squares<BF16>(gv::load4(p.base + o), acc);
-        } else {
-            for (uint64_t e = o < p.lo ? p.lo : o; e < o + 16 && e < p.hi; e += ES)
-                acc[0] = square_to(acc[0], gv::load_elem<BF16>(p.base + e));
-        }
+        const int32_t k = vector_at<BLOCK, BF16>(p, u, lane);
+        x[u] = u32x4{0u, 0u, 0u, 0u};
+        if (k >= 0 && k + VE <= p.n) x[u] = gv::load4_nt(p.in + static_cast<int64_t>(k) * ES);
     }
+#pragma unroll
+    for (uint32_t u = 0; u < kVecPerLane; ++u) {
+        const int32_t k = vector_at<BLOCK, BF16>(p, u, lane);
+        if ((k < 0 && k + VE > 0) || (k < p.n && k + VE > p.n)) x[u] = gv::load_some<BF16, VE>(p.in, k, p.n);
+    }
+}
+
+template <int BLOCK, bool BF16>
+__device__ __forceinline__ void tile_squares(const Piece& p, uint32_t lane, double (&acc)[2]) {
+    u32x4 x[kVecPerLane];
+    load_tile<BLOCK, BF16>(p, lane, x);
+#pragma unroll
+    for (uint32_t u = 0; u < kVecPerLane; ++u) add_squares<BF16>(x[u], acc);
 }
 
 template <int BLOCK>
@@ -236,36 +260,37 @@ __device__ __forceinline__ u32x4 scaled(const u32x4& x, float c) {
     return y;
 }
 
+// out: the output piece's start.
 template <int BLOCK, bool BF16>
 __device__ __forceinline__ void tile_scaled(const Piece& p, char* out, uint32_t lane, float c) {
-    constexpr uint32_t ES = BF16 ? 2 : 4;
-    if (p.at >= p.lo && p.at + tile_bytes(BLOCK) <= p.hi) {
-        u32x4 x[kVecPerLane];
-#pragma unroll
-        for (uint32_t u = 0; u < kVecPerLane; ++u) x[u] = gv::load4_nt(p.base + p.at + (u * BLOCK + lane) * 16u);
+    constexpr int VE = BF16 ? 8 : 4;
+    constexpr int64_t ES = BF16 ? 2 : 4;
+    u32x4 x[kVecPerLane];
+    load_tile<BLOCK, BF16>(p, lane, x);
+    if (inside<BLOCK, BF16>(p)) {
 #pragma unroll
         for (uint32_t u = 0; u < kVecPerLane; ++u)
-            gv::store4_nt(out + p.at + (u * BLOCK + lane) * 16u, scaled<BF16>(x[u], c));
+            gv::store4_nt(out + static_cast<int64_t>(vector_at<BLOCK, BF16>(p, u, lane)) * ES, scaled<BF16>(x[u], c));
         return;
     }
+#pragma unroll
     for (uint32_t u = 0; u < kVecPerLane; ++u) {
-        const uint64_t o = p.at + (u * BLOCK + lane) * 16u;
-        if (o >= p.lo && o + 16 <= p.hi) {
-            gv::store4_nt(out + o, scaled<BF16>(gv::load4(p.base + o), c));
+        const int32_t k = vector_at<BLOCK, BF16>(p, u, lane);
+        const u32x4 y = scaled<BF16>(x[u], c);
+        if (k >= 0 && k + VE <= p.n) {
+            gv::store4_nt(out + static_cast<int64_t>(k) * ES, y);
         } else {
-            for (uint64_t e = o < p.lo ? p.lo : o; e < o + 16 && e < p.hi; e += ES)
-                gv::store_elem<BF16>(out + e, gv::load_elem<BF16>(p.base + e) * c);
+            gv::store_some<BF16, VE>(out, k, p.n, y);
         }
     }
 }
 
-// out: the output tensor's start.
 template <int BLOCK>
 __device__ __forceinline__ void tile_scaled(const Piece& p, char* out, uint32_t lane, float c) {
     if (p.bf16) {
-        tile_scaled<BLOCK, true>(p, out - p.lo, lane, c);
+        tile_scaled<BLOCK, true>(p, out, lane, c);
     } else {
-        tile_scaled<BLOCK, false>(p, out - p.lo, lane, c);
+        tile_scaled<BLOCK, false>(p, out, lane, c);
     }
 }
 
@@ -277,66 +302,202 @@ __global__ __launch_bounds__(kClipBlock) void clip_kernel(ClipArgs) {
     // From the last tile back: what was read last is likeliest in cache.
     for (uint32_t back = blockIdx.x; back < tiles; back += gridDim.x) {
         const uint32_t tile = tiles - 1 - back;
-        const int t = tensor_at(a, tile);
+        const int t = piece_at(a, tile);
         tile_scaled<kClipBlock>(piece_of(a, t, tile, tile_bytes(kClipBlock)), a->out[t], threadIdx.x, c);
     }
 }
 
-// The norm, and with CLIP the scaling by it, in one workgroup.
+// ---- few small tensors ------------------------------------------------------
+//
+// One launch of one workgroup: latency counts, not bandwidth.  The host cuts
+// the tensors into tiles, so that a wave reads where its tiles are with one
+// round of scalar loads; all its data is then in flight at once, and stays in
+// registers until the norm is known and it is scaled and stored.
+
+struct SmallArgs {
+    const char* in[kSmallTiles];
+    char* out[kSmallTiles];
+    uint32_t count[kSmallTiles];    // elements, the top bit says bf16; 0 past the last tile
+    int32_t in_place;
+    float* norm;
+    float max_norm;
+};
+
+// A lane's part of a tile: the whole vectors, and for the first lanes one
+// element each of the rest.
+struct Part {
+    u32x4 x[kVecPerLane];
+    uint32_t e;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load_part(const char* in, uint32_t n, uint32_t lane, Part& p) {
+    constexpr uint32_t VE = BF16 ? 8 : 4;
+    constexpr uint32_t ES = BF16 ? 2 : 4;
+    const uint32_t vectors = n / VE;
+#pragma unroll
+    for (uint32_t u = 0; u < kVecPerLane; ++u) {
+        p.x[u] = u32x4{0u, 0u, 0u, 0u};
+        if (u * 64 + lane < vectors) p.x[u] = gv::load4(in + (u * 64 + lane) * 16u);
+    }
+    p.e = 0;
+    const uint32_t k = vectors * VE + lane;
+    if (k < n) {
+        if constexpr (BF16) {
+            p.e = *reinterpret_cast<const uint16_t*>(in + k * ES);
+        } else {
+            p.e = *reinterpret_cast<const uint32_t*>(in + k * ES);
+        }
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void add_part(const Part& p, double (&acc)[2]) {
+#pragma unroll
+    for (uint32_t u = 0; u < kVecPerLane; ++u) add_squares<BF16>(p.x[u], acc);
+    acc[0] = square_to(acc[0], __uint_as_float(BF16 ? p.e << 16 : p.e));
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_part(char* out, uint32_t n, uint32_t lane, const Part& p, float c) {
+    constexpr uint32_t VE = BF16 ? 8 : 4;
+    constexpr uint32_t ES = BF16 ? 2 : 4;
+    const uint32_t vectors = n / VE;
+#pragma unroll
+    for (uint32_t u = 0; u < kVecPerLane; ++u)
+        if (u * 64 + lane < vectors) gv::store4_nt(out + (u * 64 + lane) * 16u, scaled<BF16>(p.x[u], c));
+    const uint32_t k = vectors * VE + lane;
+    if (k < n) {
+        if constexpr (BF16) {
+            *reinterpret_cast<uint16_t*>(out + k * ES) = static_cast<uint16_t>(rr::bf16_bits(__uint_as_float(p.e << 16) * c));
+        } else {
+            *reinterpret_cast<float*>(out + k * ES) = __uint_as_float(p.e) * c;
+        }
+    }
+}
+
 template <bool CLIP>
 __global__ __launch_bounds__(kSmallBlock) void small_kernel(SmallArgs) {
-    constexpr int kWaves = kSmallBlock / 64;
     const Konst<SmallArgs> a = args<SmallArgs>();
-    const Finder<SmallArgs> find(a);
     const uint32_t lane = threadIdx.x & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t tiles = a->tiles;
+    uint32_t count[kSmallPerWave];
+    const char* in[kSmallPerWave];
+#pragma unroll
+    for (int j = 0; j < kSmallPerWave; ++j) {
+        count[j] = a->count[wave + j * kSmallWaves];
+        in[j] = a->in[wave + j * kSmallWaves];
+    }
+    Part part[kSmallPerWave];
+#pragma unroll
+    for (int j = 0; j < kSmallPerWave; ++j) {
+        if (count[j] == 0) continue;
+        if (count[j] & kBf16Bit) {
+            load_part<true>(in[j], count[j] & ~kBf16Bit, lane, part[j]);
+        } else {
+            load_part<false>(in[j], count[j], lane, part[j]);
+        }
+    }
     double acc[2] = {0.0, 0.0};
-    for (uint32_t tile = wave; tile < tiles; tile += kWaves)
-        tile_squares<64>(piece_of(a, find(tile), tile, tile_bytes(64)), lane, acc);
+#pragma unroll
+    for (int j = 0; j < kSmallPerWave; ++j) {
+        if (count[j] == 0) continue;
+        if (count[j] & kBf16Bit) {
+            add_part<true>(part[j], acc);
+        } else {
+            add_part<false>(part[j], acc);
+        }
+    }
     const float norm = static_cast<float>(__builtin_sqrt(gv::block_sum<kSmallBlock>(acc[0] + acc[1])));
     if (threadIdx.x == 0) *a->norm = norm;
     if constexpr (CLIP) {
         const float c = gv::clip_factor(norm, a->max_norm);
         if (a->in_place && c == 1.0f) return;
-        for (uint32_t tile = wave; tile < tiles; tile += kWaves) {
-            const int t = find(tile);
-            tile_scaled<64>(piece_of(a, t, tile, tile_bytes(64)), a->out[t], lane, c);
+#pragma unroll
+        for (int j = 0; j < kSmallPerWave; ++j) {
+            if (count[j] == 0) continue;
+            char* const out = a->out[wave + j * kSmallWaves];
+            if (count[j] & kBf16Bit) {
+                store_part<true>(out, count[j] & ~kBf16Bit, lane, part[j], c);
+            } else {
+                store_part<false>(out, count[j], lane, part[j], c);
+            }
         }
     }
 }
 
-// Puts tensors from `t` on into one launch's arguments until they are full;
-// returns the next tensor.  Empty tensors take no tile and no place.
+// The tiles of one tensor: each ends on a line of its input.
+int64_t small_tiles(const void* in, int64_t bytes) {
+    const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(in) % kLine);
+    return (lead + bytes + tile_bytes(64) - 1) / tile_bytes(64);
+}
+
+int launch_small(const NormLaunch& l, bool clip, const char** msg) {
+    SmallArgs a{};
+    a.in_place = 1;
+    a.norm = l.norm;
+    a.max_norm = l.max_norm;
+    int tile = 0;
+    for (int32_t t = 0; t < l.n_tensors; ++t) {
+        if (l.numels[t] == 0) continue;
+        const bool bf16 = l.dtypes[t] == DDP_BF16;
+        const int64_t bytes = l.numels[t] * (bf16 ? 2 : 4);
+        const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(l.in[t]) % kLine);
+        if (clip && l.out[t] != l.in[t]) a.in_place = 0;
+        for (int64_t at = -lead; at < bytes; at += tile_bytes(64), ++tile) {
+            const int64_t lo = std::max<int64_t>(at, 0);
+            const int64_t hi = std::min<int64_t>(at + tile_bytes(64), bytes);
+            a.in[tile] = static_cast<const char*>(l.in[t]) + lo;
+            if (clip) a.out[tile] = static_cast<char*>(l.out[t]) + lo;
+            a.count[tile] = static_cast<uint32_t>((hi - lo) / (bf16 ? 2 : 4)) | (bf16 ? kBf16Bit : 0u);
+        }
+    }
+    void* list[] = {&a};
+    const hipError_t e = hipLaunchKernel(
+        clip ? reinterpret_cast<const void*>(&small_kernel<true>) : reinterpret_cast<const void*>(&small_kernel<false>),
+        dim3(1), dim3(kSmallBlock), list, 0, static_cast<hipStream_t>(l.stream));
+    if (e == hipSuccess) return 0;
+    *msg = "hipLaunchKernel(small norm)";
+    return static_cast<int>(e);
+}
+
+// Where in a list of tensors the next launch goes on.
+struct Place {
+    int32_t t;
+    int64_t at;    // element of tensor t
+};
+
+// Puts the tensors from `from` on into one launch's arguments until they are
+// full; false when nothing was left.  Empty tensors take no place.
 template <class A>
-int32_t fill_set(const NormLaunch& l, int32_t t, uint32_t bytes, A& a) {
+bool fill_set(const NormLaunch& l, Place& from, uint32_t bytes, A& a) {
     int64_t tiles = 0;
     a.n = 0;
     a.in_place = 1;
-    for (; t < l.n_tensors && a.n < A::kCap; ++t) {
-        if (l.numels[t] == 0) continue;
-        const int64_t es = l.dtypes[t] == DDP_BF16 ? 2 : 4;
-        const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(l.in[t]) % kLine);
-        const int64_t need = (lead + l.numels[t] * es + bytes - 1) / bytes;
-        if (tiles + need > kMaxTiles) break;
-        a.in[a.n] = static_cast<const char*>(l.in[t]);
-        if constexpr (A::kOut) {
-            if (l.out != nullptr) {
-                a.out[a.n] = static_cast<char*>(l.out[t]);
-                if (l.out[t] != l.in[t]) a.in_place = 0;
+    for (; from.t < l.n_tensors && a.n < A::kCap; ++from.t, from.at = 0) {
+        const int64_t es = l.dtypes[from.t] == DDP_BF16 ? 2 : 4;
+        for (; from.at < l.numels[from.t] && a.n < A::kCap; ++a.n) {
+            const int64_t count = std::min(l.numels[from.t] - from.at, kMaxPiece);
+            const char* in = static_cast<const char*>(l.in[from.t]) + from.at * es;
+            const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(in) % kLine);
+            a.in[a.n] = in;
+            if constexpr (A::kOut) {
+                a.out[a.n] = static_cast<char*>(l.out[from.t]) + from.at * es;
+                if (a.out[a.n] != in) a.in_place = 0;
             }
+            a.count[a.n] = static_cast<uint32_t>(count) | (es == 2 ? kBf16Bit : 0);
+            a.first_tile[a.n] = static_cast<uint32_t>(tiles);
+            tiles += (lead + count * es + bytes - 1) / bytes;
+            from.at += count;
         }
-        a.numel[a.n] = static_cast<uint64_t>(l.numels[t]) | (es == 2 ? kBf16Bit : 0);
-        a.first_tile[a.n] = static_cast<uint32_t>(tiles);
-        tiles += need;
-        ++a.n;
+        if (from.at < l.numels[from.t]) break;
     }
     a.tiles = static_cast<uint32_t>(tiles);
     a.add = 0;
     a.partials = l.partials;
     a.norm = l.norm;
     a.max_norm = l.max_norm;
-    return t;
+    return a.n > 0;
 }
 
 int launch(const void* fn, unsigned grid, int block, void* arguments, unsigned lds, void* stream, const char* what,
@@ -353,14 +514,12 @@ int launch(const void* fn, unsigned grid, int block, void* arguments, unsigned l
 int launch_wide_norm(const NormLaunch& l, const char** msg) {
     NormArgs a;
     int blocks = 0;
-    for (int32_t t = 0; t < l.n_tensors;) {
-        t = fill_set(l, t, tile_bytes(kNormBlock), a);
-        if (a.n == 0) continue;
+    for (Place at = {0, 0}; fill_set(l, at, tile_bytes(kNormBlock), a);) {
         // Every launch has as many workgroups as the first, so that each adds
         // to a partial that the first one wrote.
         a.add = blocks > 0;
         if (!a.add)
-            blocks = t < l.n_tensors ? kNormPartials : static_cast<int>(std::min<uint32_t>(a.tiles, kNormPartials));
+            blocks = at.t < l.n_tensors ? kNormPartials : static_cast<int>(std::min<uint32_t>(a.tiles, kNormPartials));
         if (const int e = launch(reinterpret_cast<const void*>(&square_sum_kernel), blocks, kNormBlock, &a, 0, l.stream,
                                  "hipLaunchKernel(square_sum)", msg))
             return e;
@@ -384,38 +543,24 @@ int launch_norm_of(const double* partials, int64_t count, double* fold, float* n
     return static_cast<int>(e);
 }
 
-bool norm_is_small(int32_t n_tensors, const int64_t* numels, const int32_t* dtypes, bool clip) {
-    int64_t n = 0, bytes = 0;
-    for (int32_t t = 0; t < n_tensors; ++t) {
-        if (numels[t] == 0) continue;
-        bytes += numels[t] * (dtypes[t] == DDP_BF16 ? 2 : 4);
-        if (++n > kSmallTensors || bytes > (clip ? kSmallClipBytes : kSmallNormBytes)) return false;
-    }
-    return n > 0;
+bool norm_is_small(int32_t n_tensors, const int64_t* numels, const void* const* in, const int32_t* dtypes) {
+    int64_t tiles = 0;
+    for (int32_t t = 0; t < n_tensors && tiles <= kSmallTiles; ++t)
+        if (numels[t] > 0) tiles += small_tiles(in[t], numels[t] * (dtypes[t] == DDP_BF16 ? 2 : 4));
+    return tiles > 0 && tiles <= kSmallTiles;
 }
 
 int launch_norm(const NormLaunch& l, const char** msg) {
-    if (!norm_is_small(l.n_tensors, l.numels, l.dtypes, false)) return launch_wide_norm(l, msg);
-    SmallArgs a;
-    fill_set(l, 0, tile_bytes(64), a);
-    return launch(reinterpret_cast<const void*>(&small_kernel<false>), 1, kSmallBlock, &a, 0, l.stream,
-                  "hipLaunchKernel(small norm)", msg);
+    return l.partials == nullptr ? launch_small(l, false, msg) : launch_wide_norm(l, msg);
 }
 
 int launch_clip(const NormLaunch& l, const char** msg) {
     if (!l.norm_given) {
-        if (norm_is_small(l.n_tensors, l.numels, l.dtypes, true)) {
-            SmallArgs a;
-            fill_set(l, 0, tile_bytes(64), a);
-            return launch(reinterpret_cast<const void*>(&small_kernel<true>), 1, kSmallBlock, &a, 0, l.stream,
-                          "hipLaunchKernel(small clip)", msg);
-        }
+        if (l.partials == nullptr) return launch_small(l, true, msg);
         if (const int e = launch_wide_norm(l, msg)) return e;
     }
     ClipArgs a;
-    for (int32_t t = 0; t < l.n_tensors;) {
-        t = fill_set(l, t, tile_bytes(kClipBlock), a);
-        if (a.n == 0) continue;
+    for (Place at = {0, 0}; fill_set(l, at, tile_bytes(kClipBlock), a);) {
         const unsigned grid = std::min(a.tiles, kMaxWaveGrid);
         if (const int e = launch(reinterpret_cast<const void*>(&clip_kernel), grid, kClipBlock, &a,
                                  lds_reserve(kClipWgPerCu), l.stream, "hipLaunchKernel(clip)", msg))

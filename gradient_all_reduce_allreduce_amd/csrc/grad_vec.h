@@ -33,21 +33,40 @@ __device__ __forceinline__ u32x2 load2_nt(const char* p) { return __builtin_nont
 __device__ __forceinline__ void store4_nt(char* p, u32x4 v) { __builtin_nontemporal_store(v, (GlobalOut4)(p)); }
 __device__ __forceinline__ void store2_nt(char* p, u32x2 v) { __builtin_nontemporal_store(v, (GlobalOut2)(p)); }
 
-// One element as float32, and a float32 rounded to nearest even into one.
-template <bool BF16>
-__device__ __forceinline__ float load_elem(const char* p) {
-    if constexpr (BF16) {
-        return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
-    } else {
-        return *reinterpret_cast<const float*>(p);
+// The elements k .. k + N - 1 of a vector's lane that lie in [0, n), element 0
+// at p: the loads of a tensor's first and last vector, all in flight at once,
+// zero in the other places; and the stores.
+template <bool BF16, int N>
+__device__ __forceinline__ u32x4 load_some(const char* p, int64_t k, int64_t n) {
+    u32x4 x = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        uint32_t b = 0;
+        if (k + e >= 0 && k + e < n) {
+            if constexpr (BF16) {
+                b = *reinterpret_cast<const uint16_t*>(p + (k + e) * 2);
+            } else {
+                b = *reinterpret_cast<const uint32_t*>(p + (k + e) * 4);
+            }
+        }
+        if constexpr (BF16) {
+            x[e / 2] |= b << (16 * (e & 1));
+        } else {
+            x[e] = b;
+        }
     }
+    return x;
 }
-template <bool BF16>
-__device__ __forceinline__ void store_elem(char* p, float x) {
-    if constexpr (BF16) {
-        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(rr::bf16_bits(x));
-    } else {
-        *reinterpret_cast<float*>(p) = x;
+template <bool BF16, int N>
+__device__ __forceinline__ void store_some(char* p, int64_t k, int64_t n, const u32x4& x) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (k + e < 0 || k + e >= n) continue;
+        if constexpr (BF16) {
+            *reinterpret_cast<uint16_t*>(p + (k + e) * 2) = static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
+        } else {
+            *reinterpret_cast<uint32_t*>(p + (k + e) * 4) = x[e];
+        }
     }
 }
 

@@ -3,26 +3,28 @@
 // like launch.h.
 #pragma once
 
+#include <stddef.h>
+
 #include "launch.h"
 
 namespace ddp {
 
-// Longest tensor these calls accept: 2^36 elements, 256 GiB of float32, so
-// that a tensor's tiles are below 2^28 at the smallest tile.
-constexpr int64_t kMaxGradElems = int64_t(1) << 36;
-// Tiles of one launch, and its one-wave workgroups at most (a grid holds
-// fewer than 2^32 lanes; each workgroup walks on by the grid's size).
-constexpr int64_t kMaxTiles = int64_t(1) << 30;
+// Kernel arguments that carry the tensors' addresses stay under the 8,000
+// bytes measured to pass.
+constexpr size_t kArgBytes = 7936;
+// A longer tensor goes as several pieces of so many elements (a multiple of
+// a line for every type), so that a kernel counts elements in 32 bits.
+constexpr int64_t kMaxPiece = int64_t(1) << 30;
+// One-wave workgroups of a launch at most (a grid holds fewer than 2^32
+// lanes); each walks on by the grid's size.
 constexpr uint32_t kMaxWaveGrid = 1u << 25;
 
 // Partial sums a norm leaves in its workspace at most, one per workgroup:
 // 4 workgroups of 256 lanes per CU.
 constexpr int kNormPartials = DDP_NORM_WORKSPACE_BYTES / static_cast<int>(sizeof(double));
-// Up to so many tensors (with elements) of so many bytes together, one
-// workgroup takes the norm, and scales, in one launch.
-constexpr int kSmallTensors = 64;
-constexpr int64_t kSmallNormBytes = 512 << 10;
-constexpr int64_t kSmallClipBytes = 256 << 10;
+// Up to so many 4 KiB tiles, a tensor's first and last counting as one each:
+// one workgroup takes the norm, and scales, in one launch.
+constexpr int kSmallTiles = 64;
 // One-wave workgroups of the scaling per CU.
 constexpr int kClipWgPerCu = 12;
 
@@ -40,7 +42,7 @@ struct NormLaunch {
     void* stream;
 };
 // Whether these take the one-workgroup path, which needs no partials.
-bool norm_is_small(int32_t n_tensors, const int64_t* numels, const int32_t* dtypes, bool clip);
+bool norm_is_small(int32_t n_tensors, const int64_t* numels, const void* const* in, const int32_t* dtypes);
 int launch_norm(const NormLaunch& l, const char** msg);
 // out = in * min(1, max_norm / (norm + 1e-6)), the norm taken first unless
 // it is given.

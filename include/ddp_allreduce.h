@@ -816,7 +816,7 @@ int allreduce_multi_ring_noalloc(ddp_reduce_op op, int32_t P, int32_t chunking,
  * An infinite element gives an infinite norm, a NaN a NaN.
  *
  *   n_tensors    number of tensors, >= 1
- *   numels       HOST array [n_tensors], elements of each, 0 .. 2^36
+ *   numels       HOST array [n_tensors], elements of each, 0 .. 2^40
  *   ptrs         HOST array [n_tensors] of device pointers, each aligned to
  *                its element size (NULL allowed where numels is 0)
  *   dtypes       HOST array [n_tensors] of ddp_dtype: types may be mixed
@@ -824,11 +824,12 @@ int allreduce_multi_ring_noalloc(ddp_reduce_op op, int32_t P, int32_t chunking,
  *                grad_norm_workspace_bytes gives (NULL if 0); its contents
  *                before do not matter and after are undefined
  *   norm         device pointer to one float, receives the norm
- * Host arrays are read during the call only.  One launch for up to 64 tensors
- * of 512 KiB together, else two (more for over 380 tensors).  Calls that may run at the same time (on two streams, in
+ * Host arrays are read during the call only.  One launch for few small tensors
+ * (those without a workspace), else two (more for over
+ * 490 tensors).  Calls that may run at the same time (on two streams, in
  * two graphs) need a workspace each.
  * Errors: DDP_E_ARG (counts, NULL pointers, dtypes, a workspace that is too
- * small), DDP_E_UNSUPPORTED (a tensor over 2^36 elements), DDP_E_ALIGN, DDP_E_OVERLAP (workspace or norm inside a tensor or
+ * small), DDP_E_ALIGN, DDP_E_OVERLAP (workspace or norm inside a tensor or
  * each other), DDP_E_HIP.
  */
 int grad_norm_multi(int32_t n_tensors, const int64_t* numels, const void* const* ptrs,
@@ -837,14 +838,13 @@ int grad_norm_multi(int32_t n_tensors, const int64_t* numels, const void* const*
 
 /*
  * grad_norm_workspace_bytes -- host only: the workspace of grad_norm_multi
- * (clip = 0) or grad_clip_multi (clip nonzero) for these tensors, in *bytes: 0
- * where one workgroup does it all (up to 64 tensors with elements of
- * together 512 KiB, 256 KiB when they are scaled too), else
- * DDP_NORM_WORKSPACE_BYTES.
- * Errors: DDP_E_ARG, DDP_E_UNSUPPORTED, as for the calls.
+ * and grad_clip_multi for these tensors, in *bytes: 0 for few small ones, which
+ * one workgroup takes (64 pieces of 4 KiB at most, each tensor beginning a
+ * new one on its 128-byte line), else DDP_NORM_WORKSPACE_BYTES.
+ * Errors: DDP_E_ARG, as for the calls.
  */
-int grad_norm_workspace_bytes(int32_t n_tensors, const int64_t* numels, const int32_t* dtypes,
-                              int32_t clip, int64_t* bytes);
+int grad_norm_workspace_bytes(int32_t n_tensors, const int64_t* numels, const void* const* ptrs,
+                              const int32_t* dtypes, int64_t* bytes);
 
 /*
  * grad_clip_multi -- scale many gradient tensors so that their global
@@ -868,7 +868,7 @@ int grad_norm_workspace_bytes(int32_t n_tensors, const int64_t* numels, const in
  *   workspace    as for grad_norm_multi; not looked at when norm_given
  *   other arguments as for grad_norm_multi
  * One launch for few small tensors, else the norm's and one more (more for over
- * 272 tensors).
+ * 326 tensors).
  * Every output must be disjoint from every other buffer of the call, its own
  * input apart; the same tensor listed twice is therefore refused in place.
  * Errors: as for grad_norm_multi.
@@ -946,7 +946,7 @@ int allreduce_norm_workspace_bytes(int32_t P, int32_t chunking, ddp_dtype in_dty
  * left out: w, m, v and params stay as they were (a loss that overflowed
  * does not reach the weights).
  *
- *   numels       HOST array [n_tensors], elements of each, 0 .. 2^36
+ *   numels       HOST array [n_tensors], elements of each, 0 .. 2^40
  *   grads        HOST array [n_tensors], elements of grad_dtype
  *   w, m, v      HOST arrays [n_tensors] of pointers to float32 master weights
  *                and moments, updated in place
@@ -963,8 +963,7 @@ int allreduce_norm_workspace_bytes(int32_t P, int32_t chunking, ddp_dtype in_dty
  * vectors of streams that start alike within 128 bytes are the fastest.
  * Every w, m, v and params buffer must be disjoint from every other buffer of
  * the call.
- * Errors: DDP_E_ARG, DDP_E_UNSUPPORTED (a tensor over 2^36 elements),
- * DDP_E_ALIGN, DDP_E_OVERLAP, DDP_E_HIP.
+ * Errors: DDP_E_ARG, DDP_E_ALIGN, DDP_E_OVERLAP, DDP_E_HIP.
  */
 int adamw_step_multi(int32_t n_tensors, const int64_t* numels, const void* const* grads,
                      ddp_dtype grad_dtype, float* const* w, float* const* m, float* const* v,

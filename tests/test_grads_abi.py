@@ -59,7 +59,6 @@ def refused(fn, args, status, text=None):
 LISTS = [
     (dict(numels=[200_000, -1, 7]), N.DDP_E_ARG, "negative"),
     (dict(numels=[(1 << 40) + 1, 0, 7]), N.DDP_E_ARG, "2^40"),
-    (dict(numels=[(1 << 36) + 1, 0, 7]), N.DDP_E_UNSUPPORTED, "2^36"),
     (dict(numels=[], ptrs=[], dtypes=[]), N.DDP_E_ARG, "n_tensors"),
     (dict(ptrs=[0, 0, at(2)]), N.DDP_E_ARG, "NULL"),
     (dict(ptrs=[at(0, 2), 0, at(2)]), N.DDP_E_ALIGN, "ptrs[0]"),
@@ -176,17 +175,18 @@ def test_workspace_bytes_grow_with_the_workgroups():
 
 def test_norm_workspace_bytes():
     f = ddp.grad_norm_workspace_bytes
-    kb = 256                                              # float32 elements per KiB
-    assert f([512 * kb], [ddp.F32]) == 0 and f([1024 * kb], [ddp.BF16]) == 0
-    assert f([512 * kb, 1], [ddp.F32] * 2) == ddp.NORM_WORKSPACE_BYTES
-    assert f([256 * kb], [ddp.F32], True) == 0
-    assert f([256 * kb + 1], [ddp.F32], True) == ddp.NORM_WORKSPACE_BYTES
-    assert f([1] * 64 + [0], [ddp.F32] * 65) == 0
-    assert f([1] * 65, [ddp.F32] * 65) == ddp.NORM_WORKSPACE_BYTES
+    tile = 4096
+    assert f([64 * tile // 4], [at(0)], [ddp.F32]) == 0 and f([64 * tile // 2], [at(0)], [ddp.BF16]) == 0
+    assert f([64 * tile // 4 + 1], [at(0)], [ddp.F32]) == ddp.NORM_WORKSPACE_BYTES
+    # off a line by one element: one piece more
+    assert f([64 * tile // 4], [at(0, 4)], [ddp.F32]) == ddp.NORM_WORKSPACE_BYTES
+    assert f([64 * tile // 4 - 1], [at(0, 4)], [ddp.F32]) == 0
+    assert f([1] * 64 + [0], [at(k) for k in range(65)], [ddp.F32] * 65) == 0
+    assert f([1] * 65, [at(k) for k in range(65)], [ddp.F32] * 65) == ddp.NORM_WORKSPACE_BYTES
     with pytest.raises(DdpError):
-        f([-1], [ddp.F32])
+        f([-1], [at(0)], [ddp.F32])
     with pytest.raises(DdpError):
-        f([1], [3])
+        f([1], [at(0)], [3])
 
 
 def test_python_refusals():
