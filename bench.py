@@ -449,6 +449,17 @@ def _w_step_b(ctx):
                      "one ring of buckets x 8 chunks: 2(P-1) launches for them and 2(P-1) for the tail")
 
 
+@work("allreduce-norm-resnet50-bucketed", "resnet")
+def _w_norm_resnet(ctx):
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, rows = _resnet(ctx)
+    return Work("resnet50 p8 f32 mean with the result's global norm, all buckets in one bucketed call",
+                lambda i: ddp.allreduce_norm(rows[i % 2][0], "mean", 8, out=rows[i % 2][1],
+                                             bucket_elems=plan.bucket_elems),
+                8 * plan.total * 8, "ring_norm_kernel<8, false, false>",
+                note="the bits of ring-resnet50-bucketed; a second launch adds the workgroups' sums")
+
+
 @work("multi-resnet50", "resnet_tensors")
 def _w_multi(ctx):
     import torch
@@ -547,6 +558,25 @@ def _w_multi_sgd(ctx):
     return Work("resnet50 p8 f32 mean, 161 separate tensors, one launch with fused sgd-momentum per tensor",
                 lambda i: run(1e-3, 0.9, "mean"), 8 * plan.total * 4 + 16 * plan.total,
                 "multi_ring_kernel<8, false, false, true>", 1)
+
+
+@work("grad-norm-resnet50", "resnet_tensors")
+def _w_grad_norm(ctx):
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, tensors = _resnet_tensors(ctx)
+    grads = [ddp.MultiGrad(ts) for ts in tensors]
+    return Work("resnet50 f32, global norm of 161 separate tensors (one rank's; the ranks in turn)",
+                lambda i: grads[i % 8].norm(), plan.total * 4, "square_sum_kernel", 2, host_timing=True)
+
+
+@work("clip-resnet50", "resnet_tensors")
+def _w_clip(ctx):
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, tensors = _resnet_tensors(ctx)
+    runs = [ddp.MultiGrad(tensors[r]).bind_clip(out=tensors[r + 4]) for r in range(4)]
+    return Work("resnet50 f32, 161 separate tensors clipped to norm 1 into another set, the norm in the same call",
+                lambda i: runs[i % 4](1.0), plan.total * 8, None, 3, host_timing=True,
+                note="the tensors are read twice, for the norm and for the scaling")
 
 
 def _packed(ctx, key):
@@ -682,6 +712,59 @@ def _w_zero1_b(ctx):
                 8 * plan.total * 4 + 16 * plan.total, RING_SGD_BF16,
                 ddp.ddp_buckets_launch_count(8, 8, ddp.BF16, ddp.BF16, True, plan.total, plan.bucket_elems),
                 note="every bucket its own ring, the same bits")
+
+
+@work("allreduce-norm-vitb16-one-copy", "vit")
+def _w_norm_vit(ctx):
+    import torch
+
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, rows, _, _ = _vit(ctx)
+    out = torch.empty(plan.total, device=_dev())
+    return Work("vitb16 p8 bf16 mean into one float32 copy with its global norm, all buckets in one bucketed call",
+                lambda i: ddp.allreduce_norm(rows[i % 2][0], "mean", 8, out=[out], bucket_elems=plan.bucket_elems),
+                plan.total * (8 * 2 + 4), "ring_norm_kernel<8, true, false>")
+
+
+def _vit_adamw(ctx):
+    """AdamW state of the ViT-B/16 set in bucket order, and its step on a
+    float32 gradient, clipped by a norm, with a bf16 copy of the weights."""
+    import torch
+
+    import gradient_all_reduce_allreduce_amd as ddp
+    import workloads
+    plan = _vit(ctx)[0]
+    w, m, v = plan.alloc_state(3)
+    workloads.torch_normal_(w, 0.02, seed=7)
+    m.zero_()
+    v.zero_()
+    grad = workloads.torch_normal_(torch.empty(plan.total, device=_dev()), 1e-3, seed=8)
+    params = torch.empty(plan.total, dtype=torch.bfloat16, device=_dev())
+    return grad, ddp.MultiGrad(grad).bind_adamw(w, m, v, params)
+
+
+@work("adamw-vitb16", "vit")
+def _w_adamw(ctx):
+    import torch
+    plan = _vit(ctx)[0]
+    _, step = _vit_adamw(ctx)
+    norm = torch.full((), 9.3, device=_dev())
+    return Work("vitb16 f32 gradient (flat), clipped AdamW step on fp32 w, m, v with a bf16 copy of the weights",
+                lambda i: step(1e-3, i + 1, norm=norm, max_norm=1.0), plan.total * (4 + 24 + 2),
+                "adamw_kernel<16, false, 2>", 1)
+
+
+@work("train-step-vitb16", "vit")
+def _w_train_step(ctx):
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, rows, _, _ = _vit(ctx)
+    grad, step = _vit_adamw(ctx)
+
+    def run(i):
+        _, norm = ddp.allreduce_norm(rows[i % 2][0], "mean", 8, out=[grad], bucket_elems=plan.bucket_elems)
+        step(1e-3, i + 1, norm=norm, max_norm=1.0)
+    return Work("vitb16 p8 bf16: mean into one float32 copy with its norm, then AdamW clipped by it, bf16 weights out",
+                run, plan.total * (8 * 2 + 4 + 4 + 24 + 2), None, 3)
 
 
 @work("packed-step-ragged2000", "ragged")

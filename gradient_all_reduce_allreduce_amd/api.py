@@ -1003,25 +1003,26 @@ def allreduce_norm(tensors, op="sum", chunking=None, out=None, out_dtype=None, b
         dt = out_dtype or tensors[0].dtype
         out = [torch.empty(tensors[0].shape, dtype=dt, device=tensors[0].device) for _ in range(P)]
     out = _rank_tensors(out, "allreduce_norm out")
-    if len(out) not in (1, P) or out[0].numel() != tensors[0].numel():
+    x, y = tensors[0], out[0]
+    n, index = x.numel(), x.get_device()
+    if len(out) not in (1, P) or y.numel() != n:
         raise ValueError("allreduce_norm: out must match the inputs, P tensors or one")
-    _same_device(tensors, out, "allreduce_norm")
-    device = tensors[0].device
-    n = tensors[0].numel()
-    icode, ocode = torch_dtype_code(tensors[0].dtype), torch_dtype_code(out[0].dtype)
-    C = chunking or P
+    if y.get_device() != index:
+        raise ValueError("allreduce_norm: outputs must live on the inputs' device")
     if bucket_elems is not None and bucket_elems < 1:
         raise ValueError("allreduce_norm: bucket_elems must be at least 1")
-    need = _norm_workspace(P, C, icode, ocode, n, bucket_elems or 0)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
             return allreduce_norm(tensors, op, chunking, out, out_dtype, bucket_elems)
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    norm = torch.empty((), dtype=torch.float32, device=device)
-    ins, outs = [t.data_ptr() for t in tensors], [t.data_ptr() for t in out]
-    end = (norm.data_ptr(), ws.data_ptr(), need, _raw_stream(device.index))
+    icode, ocode = torch_dtype_code(x.dtype), torch_dtype_code(y.dtype)
+    C = chunking or P
+    need = _norm_workspace(P, C, icode, ocode, n, bucket_elems or 0)
+    ws = x.new_empty(need, dtype=torch.uint8)
+    norm = x.new_empty((), dtype=torch.float32)
+    args = [op, P, C, [t.data_ptr() for t in tensors], icode, [t.data_ptr() for t in out], ocode, n]
+    end = (norm.data_ptr(), ws.data_ptr(), need, _raw_stream(index))
     if bucket_elems is not None:
-        allreduce_ring_norm_buckets(op, P, C, ins, icode, outs, ocode, n, bucket_elems, *end)
+        allreduce_ring_norm_buckets(*args, bucket_elems, *end)
     else:
-        allreduce_ring_norm(op, P, C, ins, icode, outs, ocode, n, *end)
+        allreduce_ring_norm(*args, *end)
     return out, norm

@@ -176,6 +176,7 @@ def test_clip(sizes, dtype):
     src, dst = Arena(arrays, types, gap=3), Arena([np.zeros_like(a) for a in arrays], types, gap=5)
     norm = ddp.clip_grads(src.views, half, out=dst.views)
     check_norm(norm, arrays)
+    assert torch.equal(norm, ddp.grad_norm(src.views)), "the norm's own call gives the same bits"
     want = clipped(arrays, types, np.float32(float(norm)), half)
     same(dst.host(), want, "out")
     same(src.host(), arrays, "inputs")
@@ -199,6 +200,25 @@ def test_clip_below_the_limit_keeps_every_bit(dtype, inplace):
     for limit in (1e9, float("inf")):
         ddp.clip_grads(ts, limit, out=out)
         same([t.float().cpu().numpy() for t in out or ts], arrays)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_clip_of_subnormal_values(dtype):
+    """Values over the whole exponent range: products that underflow are
+    rounded into the subnormals, not flushed."""
+    rng = np.random.default_rng(3)
+    a = (rng.standard_normal(9001) * np.exp2(rng.integers(-149, -90, 9001))).astype(np.float32)
+    if dtype == "bf16":
+        a = oracle.bf16_bits_to_f32(oracle.f32_to_bf16_bits(a))
+    for n in (9001, 400_000):            # one workgroup, and many
+        arrays, types = [np.resize(a, n)], [dtype]
+        ts = separate(arrays, types)
+        ddp.clip_grads(ts, 1.0, norm=torch.tensor(3.7, device=DEV))
+        same([t.float().cpu().numpy() for t in ts], clipped(arrays, types, np.float32(3.7), 1.0))
+        ts = separate(arrays, types)
+        norm = ddp.clip_grads(ts, 1e-30)
+        check_norm(norm, arrays)
+        same([t.float().cpu().numpy() for t in ts], clipped(arrays, types, np.float32(float(norm)), 1e-30))
 
 
 def test_clip_special_norms():
@@ -358,6 +378,24 @@ def test_adamw_special_values():
         same([x.cpu().numpy() for x in st], [x[0] for x in want])
 
 
+def test_adamw_over_the_whole_exponent_range():
+    """Gradients and state from subnormal to huge: subnormals are kept, the
+    division and root are rounded correctly everywhere."""
+    rng = np.random.default_rng(9)
+    n = 50_000
+
+    def wide(lo, hi):
+        return (rng.standard_normal(n) * np.exp2(rng.integers(lo, hi, n))).astype(np.float32)
+    g, w, m = wide(-149, 60), wide(-149, 100), wide(-149, 100)
+    v = np.abs(wide(-149, 100))
+    for eps in (1e-8, 0.0, 1e-40):
+        st = [torch.from_numpy(x.copy()).to(DEV) for x in (w, m, v)]
+        h = dict(H, eps=eps)
+        adamw_run(ddp.MultiGrad(torch.from_numpy(g).to(DEV)).bind_adamw(*st), 3, torch.tensor(2.5, device=DEV), 1.0, h)
+        want = adamw_want([g], [w], [m], [v], oracle.clip_factor(np.float32(2.5), 1.0), 3, h)
+        same([x.cpu().numpy() for x in st], [x[0] for x in want], f"eps {eps}")
+
+
 def test_adamw_refusals():
     x = [torch.zeros(8, device=DEV) for _ in range(4)]
     mg = ddp.MultiGrad(x[0])
@@ -458,6 +496,51 @@ def test_allreduce_norm_many_partials():
     want = oracle_ring(X, "mean", P, in_dtype="bf16", out_dtype="f32")
     assert_same_bits(to_host(out), want)
     check_norm(norm, [want[0]])
+
+
+def test_allreduce_norm_over_several_launches():
+    """2^29 + 777 elements go out as two launches whose partial sums lie
+    behind each other; the outputs are the plain call's."""
+    P, n = 2, 2 ** 29 + 777
+    rows = []
+    for r in range(P):
+        x = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+        x[::4097] = float(r + 1)
+        x[-5:] = 3.0
+        rows.append(x)
+    one = torch.empty(n, device=DEV)
+    _, norm = ddp.allreduce_norm(rows, "sum", P, out=[one])
+    want = torch.empty(n, device=DEV)
+    ddp.allreduce(rows, "sum", P, out=[want, torch.empty(n, device=DEV)])
+    assert torch.equal(one, want)
+    exact = float(one.double().square().sum().sqrt())
+    assert abs(float(norm) - exact) <= 2.0 ** -24 * exact * (1 + 1e-6)
+
+
+def test_allreduce_norm_replayed():
+    """A captured call (two launches, the second counting its workgroups from
+    a word the first clears) replayed with new gradients, eager calls of the
+    same sizes between."""
+    P, n = 4, 256 * 5000 + 3
+    rows = [torch.empty(n, device=DEV) for _ in range(P)]
+    one = torch.empty(n, device=DEV)
+    for r in rows:
+        r.normal_()
+    ddp.allreduce_norm(rows, "mean", P, out=[one])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        _, norm = ddp.allreduce_norm(rows, "mean", P, out=[one])
+    for t in range(1, 5):
+        for r in rows:
+            r.normal_().mul_(t)
+        graph.replay()
+        got = one.clone(), norm.clone()
+        out, eager = ddp.allreduce_norm(rows, "mean", P)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], out[0]) and torch.equal(got[0], out[P - 1])
+        assert torch.equal(got[1], eager)
+        check_norm(eager, [out[0].cpu().numpy()])
 
 
 def test_allreduce_norm_nothing_and_not_finite():
