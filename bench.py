@@ -751,7 +751,7 @@ def _w_adamw(ctx):
     norm = torch.full((), 9.3, device=_dev())
     return Work("vitb16 f32 gradient (flat), clipped AdamW step on fp32 w, m, v with a bf16 copy of the weights",
                 lambda i: step(1e-3, i + 1, norm=norm, max_norm=1.0), plan.total * (4 + 24 + 2),
-                "adamw_kernel<16, false, 2>", 1)
+                "adamw_kernel<false, 2>", 1)
 
 
 @work("train-step-vitb16", "vit")

@@ -15,14 +15,24 @@
 // leaves everything as it was.
 //
 // Bound by HBM: gradient, w, m and v are read once and w, m, v and the copy
-// written once, 28 or 32 bytes an element, against some forty instructions
-// (a correctly rounded division and square root among them).
+// written once (28 bytes an element with bf16 gradient and copy), against some
+// forty instructions, a correctly rounded division and square root among them.
+// 86.6M elements, bf16 gradient and copy: 370 us, 6.5 TB/s; 658M: 2.79 ms, 6.6.
 //
-// Layout: tiles of kTileElems elements that start on the lines of w (the
-// first of a tensor whose w starts inside a line is short), every lane 4
-// consecutive elements of each stream; the other streams usually lie the
-// same way and are read as they lie if not.  Addresses and sizes travel in the
-// kernel arguments, several launches for more tensors than fit.
+// Layout: one one-wave workgroup per tile of 256 elements, a tile starting on
+// a line of w (a tensor's first one is short when its w starts inside a line),
+// every lane 4 consecutive elements of each stream; the other streams usually
+// lie the same way and are read as they lie if not.  With as many workgroups as
+// tiles and few of them on a CU the mix of four streams in and four out moves
+// as the all-reduce's does (launch.h): workgroups of 256 that walk over many
+// tiles took 492 us instead of 370, and by the cap on one-wave workgroups per CU
+// 8: 421, 10: 381, 12: 373, 14: 382, 16: 381, 20: 400, none: 394 us.
+// A new workgroup's way to its first load is the search for its tensor and one
+// batch of scalar loads; what the step needs besides (the norm, the step's
+// number, divisions, two powers) is worked out while the data is in flight.
+// (The norm and the count read as vector loads waited for the tile's data first:
+// 463 us with the count on the GPU, 378 now.)  Addresses and sizes travel in
+// the kernel arguments, several launches for more tensors than fit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -40,21 +50,18 @@ using rr::u32x4;
 constexpr int kBlock = 64;                             // one wave
 constexpr uint32_t kTileElems = kBlock * 4;
 constexpr uint32_t kLineElems = 32;                    // float32 per 128-byte line
-// Tensors (or pieces of them) per launch: as many as the arguments hold, or
-// few, whose arguments are quicker to hand over.
-constexpr int kManyTensors = 162;
-constexpr int kFewTensors = 16;
+// Tensors (or pieces of them) per launch: as many as the arguments hold.
+// (Arguments for 16 only, for calls with so few, made no difference.)
+constexpr int kCap = 162;
 
-template <int CAP>
 struct AdamWArgs {
-    static constexpr int kCap = CAP;
-    const char* g[CAP];
-    char* w[CAP];
-    char* m[CAP];
-    char* v[CAP];
-    char* p[CAP];
-    uint32_t count[CAP];     // elements, up to kMaxPiece
-    uint32_t first_tile[CAP];
+    const char* g[kCap];
+    char* w[kCap];
+    char* m[kCap];
+    char* v[kCap];
+    char* p[kCap];
+    uint32_t count[kCap];     // elements, up to kMaxPiece
+    uint32_t first_tile[kCap];
     int32_t n;
     uint32_t tiles;          // of all pieces
     const float* norm;
@@ -68,9 +75,8 @@ struct AdamWArgs {
     float step_size;
     float root2;
 };
-static_assert(sizeof(AdamWArgs<kManyTensors>) <= kArgBytes, "kernel arguments");
-template <int CAP>
-using KAdamW = const __attribute__((address_space(4))) AdamWArgs<CAP>*;
+static_assert(sizeof(AdamWArgs) <= kArgBytes, "kernel arguments");
+typedef const __attribute__((address_space(4))) AdamWArgs* KAdamW;
 
 // What depends on the step's number: lr / (1 - b1^t) and 1 / sqrt(1 - b2^t),
 // the powers by squaring, all float64, rounded to float32 once.
@@ -114,8 +120,7 @@ __device__ __forceinline__ void adamw_element(float g, float& w, float& m, float
 
 // The factors from the arguments and the norm and step count they point to.
 // False: the step is left out.
-template <int CAP>
-__device__ __forceinline__ bool factors(KAdamW<CAP> a, float norm, int64_t t, Factors& f) {
+__device__ __forceinline__ bool factors(KAdamW a, float norm, int64_t t, Factors& f) {
     f.c = 1.0f;
     if (a->norm != nullptr) {
         if (!(__builtin_fabsf(norm) < __builtin_inff())) return false;
@@ -139,9 +144,9 @@ __device__ __forceinline__ bool factors(KAdamW<CAP> a, float norm, int64_t t, Fa
 }
 
 // GB: bf16 gradients.  PM: the copy, 0 none, 1 float32, 2 bf16.
-template <int CAP, bool GB, int PM>
-__global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs<CAP>) {
-    const KAdamW<CAP> a = (KAdamW<CAP>)(__builtin_amdgcn_kernarg_segment_ptr());
+template <bool GB, int PM>
+__global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs) {
+    const KAdamW a = (KAdamW)(__builtin_amdgcn_kernarg_segment_ptr());
     const uint32_t tiles = a->tiles;
     const float norm = a->norm != nullptr ? gv::load_uniform(a->norm) : 0.0f;
     const int64_t step = a->step != nullptr ? gv::load_uniform(a->step) : 1;
@@ -211,22 +216,22 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AdamWArgs<CAP>) {
     }
 }
 
-template <int CAP>
 const void* kernel_for(const AdamWLaunch& l) {
     const int pm = l.params == nullptr ? 0 : (l.param_bf16 ? 2 : 1);
     if (l.grad_bf16) {
-        return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, true, 0>)
-               : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, true, 1>)
-                         : reinterpret_cast<const void*>(&adamw_kernel<CAP, true, 2>);
+        return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<true, 0>)
+               : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<true, 1>)
+                         : reinterpret_cast<const void*>(&adamw_kernel<true, 2>);
     }
-    return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, false, 0>)
-           : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<CAP, false, 1>)
-                     : reinterpret_cast<const void*>(&adamw_kernel<CAP, false, 2>);
+    return pm == 0 ? reinterpret_cast<const void*>(&adamw_kernel<false, 0>)
+           : pm == 1 ? reinterpret_cast<const void*>(&adamw_kernel<false, 1>)
+                     : reinterpret_cast<const void*>(&adamw_kernel<false, 2>);
 }
 
-template <int CAP>
-int launch_all(const AdamWLaunch& l, const char** msg) {
-    AdamWArgs<CAP> a;
+}  // namespace
+
+int launch_adamw(const AdamWLaunch& l, const char** msg) {
+    AdamWArgs a;
     a.norm = l.norm;
     a.max_norm = l.max_norm;
     a.step = l.step_dev;
@@ -246,11 +251,11 @@ int launch_all(const AdamWLaunch& l, const char** msg) {
         a.step_size = s.size;
         a.root2 = s.root2;
     }
-    const void* fn = kernel_for<CAP>(l);
+    const void* fn = kernel_for(l);
     int64_t at = 0;   // element of tensor t that the next piece starts at
     for (int32_t t = 0; t < l.n_tensors;) {
         int64_t tiles = 0;
-        for (a.n = 0; t < l.n_tensors && a.n < CAP;) {
+        for (a.n = 0; t < l.n_tensors && a.n < kCap;) {
             const int64_t count = std::min(l.numels[t] - at, kMaxPiece);
             if (count > 0) {
                 const int64_t ges = l.grad_bf16 ? 2 : 4;
@@ -284,12 +289,6 @@ int launch_all(const AdamWLaunch& l, const char** msg) {
         }
     }
     return 0;
-}
-
-}  // namespace
-
-int launch_adamw(const AdamWLaunch& l, const char** msg) {
-    return l.n_tensors <= kFewTensors ? launch_all<kFewTensors>(l, msg) : launch_all<kManyTensors>(l, msg);
 }
 
 }  // namespace ddp

@@ -20,7 +20,23 @@
 // partials of the earlier.
 //
 // Bound by HBM: the norm reads every element once, the scaling reads and
-// writes it once.
+// writes it once, and all of them are needed before the first can be scaled: a
+// set larger than the caches is read twice.  What carries each kernel:
+//   * the norm: 1,024 workgroups of 256 lanes take every 1,024th tile of 16
+//     KiB, four non-temporal 16-byte loads a lane in flight.  2.0B bf16
+//     elements 580 us, 7.0 TB/s; 86.6M 29 us.  With ordinary loads 6.0 TB/s; a
+//     contiguous run of tiles per workgroup 7% slower; 2,048 workgroups 4%.
+//     2,048 one-wave workgroups reach 7.2 TB/s on the 2.0B elements, but lose
+//     5% on 86.6M and 3% on ragged sets.
+//   * the scaling: one one-wave workgroup per 4 KiB tile, 12 of them on a CU.
+//     300M float32 370 us, 6.5 TB/s; 2,048 workgroups of 256 walking over the
+//     tiles 5.1 TB/s.  It starts from the last tile.  (Reading the end of the
+//     set for the norm with loads meant to stay in cache changed nothing.)
+//   * few small tensors: one launch of one workgroup for norm and scaling.
+//     24 tensors of 1,000 float32: norm 2.7 us on the GPU and 6.1 a call against
+//     4.0 and 9.2 for the wide kernels, clip 3.9 and 6.6 against 7.6 and 13.3;
+//     at the limit of 64 tiles level on the GPU (clip 7.0 against 6.1 us), a
+//     third less per call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -25,7 +25,8 @@ constexpr int kNormPartials = DDP_NORM_WORKSPACE_BYTES / static_cast<int>(sizeof
 // Up to so many 4 KiB tiles, a tensor's first and last counting as one each:
 // one workgroup takes the norm, and scales, in one launch.
 constexpr int kSmallTiles = 64;
-// One-wave workgroups of the scaling per CU.
+// One-wave workgroups of the scaling per CU, the fastest of 12, 14, 16, 20, 24
+// and no cap by up to 4%.
 constexpr int kClipWgPerCu = 12;
 
 // The global norm of n_tensors gradient tensors, and their scaling.
@@ -54,11 +55,13 @@ int launch_clip(const NormLaunch& l, const char** msg);
 // 99,832 partials (P = 8, 25.6M elements) 64 workgroups of 1,024 lanes add 3.7
 // us to the all-reduce, 256 of 256 lanes 7.7 us (each of them takes a turn
 // at the count) and one of 1,024 lanes 26 us; an empty launch adds 1.6 us.
+// On 4,000 partials one workgroup and 64 take the same.
 constexpr int64_t kNormFoldOver = 4096;
 constexpr int kNormFold = 64;
 int launch_norm_of(const double* partials, int64_t count, double* fold, float* norm, void* stream, const char** msg);
 
-// One-wave workgroups of the AdamW step per CU.
+// One-wave workgroups of the AdamW step per CU (figures in adamw.hip): the best
+// or within 2% of it for every pair of types.
 constexpr int kAdamWWgPerCu = 12;
 
 // One AdamW step on n_tensors tensors.
