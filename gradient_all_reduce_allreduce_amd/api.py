@@ -928,8 +928,8 @@ class MultiGrad:
         per gradient, updated in place), writing the new weights also to
         ``params`` (float32 or bfloat16) if given.  ``step``: the step's
         number from 1, an int or a tensor of one int64 on the GPU (read when
-        the step runs, so that a captured step can be replayed).  With
-        ``norm`` (a float32 scalar tensor) and ``max_norm`` the gradient is
+        the step runs, so that a captured step can be replayed; ``lr`` and the
+        other numbers are taken at the call).  With ``norm`` (a float32 scalar tensor) and ``max_norm`` the gradient is
         clipped on the way, and a norm that is not finite leaves the step
         out.  The gradients must all have one type."""
         import torch

@@ -30,8 +30,10 @@
 //     5% on 86.6M and 3% on ragged sets.
 //   * the scaling: one one-wave workgroup per 4 KiB tile, 12 of them on a CU.
 //     300M float32 370 us, 6.5 TB/s; 2,048 workgroups of 256 walking over the
-//     tiles 5.1 TB/s.  It starts from the last tile.  (Reading the end of the
-//     set for the norm with loads meant to stay in cache changed nothing.)
+//     tiles 5.1 TB/s, two tiles a workgroup 6.3.  In place with c = 1 it has
+//     nothing to do but start: 63 us.  It begins with the last tile.
+//     (Reading the end of the set for the norm with loads meant to stay in
+//     cache changed nothing.)
 //   * few small tensors: one launch of one workgroup for norm and scaling.
 //     24 tensors of 1,000 float32: norm 2.7 us on the GPU and 6.1 a call against
 //     4.0 and 9.2 for the wide kernels, clip 3.9 and 6.6 against 7.6 and 13.3;

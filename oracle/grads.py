@@ -16,10 +16,9 @@ Two forms of each: in float64, the definition; and in float32 with one
 rounding per operation and the scalar factors rounded from float64 once,
 which is what the HIP kernels are held to bit for bit.
 
-Parity status: the float64 forms are pinned by the tests against
-torch.nn.utils.clip_grad_norm_ and torch.optim.AdamW run in float64, and the
-float32 forms against the float64 ones within bounds derived from the count
-of roundings.
+Parity status: the float64 forms are pinned by the tests against PyTorch's
+own clipping and AdamW run in float64, and the float32 forms against the
+float64 ones within bounds derived from the count of roundings.
 """
 
 import numpy as np
