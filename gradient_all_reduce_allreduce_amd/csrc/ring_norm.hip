@@ -24,7 +24,7 @@ __device__ __forceinline__ KRingNorm norm_args() {
     return (KRingNorm)(__builtin_amdgcn_kernarg_segment_ptr());
 }
 
-// Leaves the wave's sum.  The first workgroup of a call also clears the count
+// Leaves the wave's sum.  The first workgroup of a launch also clears the count
 // that the partials' sum starts from (grad_norm.hip).
 __device__ __forceinline__ void leave(KRingNorm a, double sq) {
     sq = gv::wave_sum63(sq);
