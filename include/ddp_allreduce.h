@@ -51,9 +51,10 @@
  *     touch one more line, and every wave store leave two lines partly
  *     written (measured 19% slower for gradient rows 32 bytes into a line,
  *     8-11% for the fused step's momentum).  The tensors of
- *     pack/unpack need only their element type's alignment; pack/unpack take
- *     their segment table and tensor addresses as host arrays and check
- *     them.  The multi-tensor calls read device tables (the tile plan and
+ *     pack/unpack, and those of the gradient norm, clipping and AdamW calls,
+ *     need only their element type's alignment; these calls take
+ *     their segment table, sizes and tensor addresses as host arrays and check
+ *     them.  The multi-tensor all-reduce calls read device tables (the tile plan and
  *     the tensors' addresses) that the library cannot read on the host:
  *     their contents are the caller's responsibility.
  *   - Two buffers of one call named in host arrays may either be disjoint or

@@ -575,6 +575,51 @@ def test_on_another_stream_and_two_at_once():
     same([o.cpu().numpy() for o in out], clipped(arrays, types, np.float32(float(want)), 0.5))
 
 
+def test_with_another_gpu_current(monkeypatch):
+    """A call that finds another GPU current makes the tensors' one current
+    for its launches (seen from one GPU: the first question is answered
+    wrongly, the results are the same)."""
+    arrays, types = draw([300_000, 5], "f32")
+    g = separate(arrays, types)
+    w, m, v = state(arrays, 90)
+    st = [separate(x, types) for x in (w, m, v)]
+    mg = ddp.MultiGrad(g)
+    out = [torch.empty_like(x) for x in g]
+    clip, step = mg.bind_clip(out), mg.bind_adamw(*st)
+    rows = [torch.ones(1000, device=DEV) for _ in range(2)]
+    real, wrong, asked = torch.cuda.current_device, [], []
+
+    def current():
+        asked.append(bool(wrong))
+        return wrong.pop() if wrong else real()
+    monkeypatch.setattr(torch.cuda, "current_device", current)
+    norms = []
+    for call in (mg.norm, lambda: clip(0.5), lambda: adamw_run(step, 2), lambda: ddp.allreduce_norm(rows)[1]):
+        wrong.append(real() + 1)
+        norms.append(call())
+        assert not wrong and asked[-1] is False
+    monkeypatch.undo()
+    check_norm(norms[0], arrays)
+    assert torch.equal(norms[0], norms[1]) and float(norms[3]) == np.float32(np.sqrt(4000.0))
+    same([x.cpu().numpy() for x in out], clipped(arrays, types, np.float32(float(norms[1])), 0.5))
+    same([x.cpu().numpy() for x in st[0]], adamw_want(arrays, w, m, v, np.float32(1), 2)[0])
+
+
+def test_allreduce_norm_same_bits_at_every_cap():
+    """The cap on resident workgroups is a launch shape: outputs and norm keep
+    their bits."""
+    X = rank_draw(8, 300_007, "bf16", seed=11)
+    first = None
+    try:
+        for cap in (-1, 0, 2, 7, 16):
+            ddp.ddp_set_wg_per_cu("ring", cap)
+            out, norm = ddp.allreduce_norm(to_device(X, "bf16"), "mean", 8, out_dtype=torch.float32)
+            first = first or (out[3], norm)
+            assert torch.equal(out[3], first[0]) and torch.equal(norm, first[1])
+    finally:
+        ddp.ddp_set_wg_per_cu("ring", -1)
+
+
 def test_graphs_replayed_between_eager_calls():
     """Two graphs of the same MultiGrad, each a clip and a step whose count
     lives on the GPU, replayed in turn with eager calls between."""
