@@ -904,22 +904,26 @@ class MultiGrad:
                 raise ValueError("clip out: every output must have its gradient's type")
 
         def run(max_norm, norm=None):
-            if torch.cuda.current_device() != self._index:
-                with torch.cuda.device(self._index):
-                    return run(max_norm, norm)
-            given, ws = norm is not None, None
-            if given:
-                _scalar(norm, torch.float32, self.device, "norm")
-            else:
-                norm = self._new_norm()
-                ws = self._workspace()
-            _check(N.lib().grad_clip_multi(*self._list, optrs, max_norm, given, norm.data_ptr(),
-                                           ws.data_ptr() if ws is not None else None, self._bytes,
-                                           _raw_stream(self._index)))
-            return norm
+            return self._clip(optrs, max_norm, norm)
 
         run.tensors = (self.grads, out)
         return run
+
+    def _clip(self, optrs, max_norm, norm):
+        import torch
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._clip(optrs, max_norm, norm)
+        given, ws = norm is not None, None
+        if given:
+            _scalar(norm, torch.float32, self.device, "norm")
+        else:
+            norm = self._new_norm()
+            ws = self._workspace()
+        _check(N.lib().grad_clip_multi(*self._list, optrs, max_norm, given, norm.data_ptr(),
+                                       ws.data_ptr() if ws is not None else None, self._bytes,
+                                       _raw_stream(self._index)))
+        return norm
 
     def bind_adamw(self, w, m, v, params=None):
         """Returns ``run(lr, step, betas=(0.9, 0.999), eps=1e-8,
@@ -939,7 +943,6 @@ class MultiGrad:
         w, wptrs = self._match(w, "adamw w", (torch.float32,))
         m, mptrs = self._match(m, "adamw m", (torch.float32,))
         v, vptrs = self._match(v, "adamw v", (torch.float32,))
-        count, numels, ptrs, _ = self._list
         pptrs, pcode = None, F32
         if params is not None:
             params, pptrs = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
@@ -947,23 +950,29 @@ class MultiGrad:
                 raise ValueError("adamw: params must all have the same element type")
             pcode = torch_dtype_code(params[0].dtype)
 
+        lists = (gcode, wptrs, mptrs, vptrs, pptrs, pcode)
+
         def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
-            if (norm is None) != (max_norm is None):
-                raise ValueError("adamw: norm and max_norm come together")
-            if torch.cuda.current_device() != self._index:
-                with torch.cuda.device(self._index):
-                    return run(lr, step, betas, eps, weight_decay, norm, max_norm)
-            step_dev = norm_dev = None
-            if isinstance(step, torch.Tensor):
-                step_dev, step = _scalar(step, torch.int64, self.device, "step").data_ptr(), 0
-            if norm is not None:
-                norm_dev = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
-            _check(N.lib().adamw_step_multi(count, numels, ptrs, gcode, wptrs, mptrs, vptrs, pptrs, pcode, lr,
-                                            betas[0], betas[1], eps, weight_decay, step, step_dev, norm_dev,
-                                            max_norm or 0.0, _raw_stream(self._index)))
+            self._adamw(lists, lr, step, betas, eps, weight_decay, norm, max_norm)
 
         run.tensors = (self.grads, w, m, v, params)
         return run
+
+    def _adamw(self, lists, lr, step, betas, eps, weight_decay, norm, max_norm):
+        import torch
+        if (norm is None) != (max_norm is None):
+            raise ValueError("adamw: norm and max_norm come together")
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._adamw(lists, lr, step, betas, eps, weight_decay, norm, max_norm)
+        step_dev = norm_dev = None
+        if isinstance(step, torch.Tensor):
+            step_dev, step = _scalar(step, torch.int64, self.device, "step").data_ptr(), 0
+        if norm is not None:
+            norm_dev = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
+        count, numels, ptrs, _ = self._list
+        _check(N.lib().adamw_step_multi(count, numels, ptrs, *lists, lr, betas[0], betas[1], eps, weight_decay, step,
+                                        step_dev, norm_dev, max_norm or 0.0, _raw_stream(self._index)))
 
 
 def grad_norm(grads):

@@ -1,0 +1,89 @@
+"""The Python handles of the gradient norm, clipping and AdamW calls on the
+host: what they keep alive, and which memory they pass on.  CPU tensors stand
+in for GPU ones and a stub for the library's launching calls."""
+
+import gc
+import weakref
+
+import pytest
+import torch
+
+ddp = pytest.importorskip("gradient_all_reduce_allreduce_amd")
+from gradient_all_reduce_allreduce_amd import _native as N  # noqa: E402
+from gradient_all_reduce_allreduce_amd import api  # noqa: E402
+
+LAUNCHING = ("grad_norm_multi", "grad_clip_multi", "adamw_step_multi")
+
+
+class Gpu(torch.Tensor):
+    """A CPU tensor that says it lives on the GPU."""
+    is_cuda = True
+
+
+def gpu(n, dtype=torch.float32):
+    return torch.zeros(n, dtype=dtype).as_subclass(Gpu)
+
+
+class Lib:
+    """The library with its launching calls written down instead of made."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name in LAUNCHING:
+            return lambda *args: self.calls.append((name, args)) or N.DDP_OK
+        return getattr(self.real, name)
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    stub = Lib(N.lib())
+    monkeypatch.setattr(N, "lib", lambda: stub)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)    # a CPU tensor's device index
+    monkeypatch.setattr(api, "_raw_stream", lambda index: 0)
+    return stub
+
+
+CALLS = {
+    "norm": lambda g, s: ddp.grad_norm(g),
+    "clip": lambda g, s: ddp.clip_grads(g, 1.0),
+    "clip_into": lambda g, s: ddp.clip_grads(g, 1.0, out=s[0]),
+    "adamw": lambda g, s: ddp.adamw_step(g, *s[:3], 1e-3, 1, params=s[3]),
+    "bound_clip": lambda g, s: ddp.MultiGrad(g).bind_clip(s[0])(1.0),
+    "bound_adamw": lambda g, s: ddp.MultiGrad(g).bind_adamw(*s[:3], params=s[3])(1e-3, 1),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_nothing_outlives_a_call(lib, call):
+    """Gradients made anew at each step are freed as soon as the last
+    reference goes, without the cyclic collector."""
+    grads = [gpu(100), gpu(7)]
+    state = [[gpu(100), gpu(7)] for _ in range(4)]
+    refs = [weakref.ref(t) for t in grads + sum(state, [])]
+    gc.collect()
+    gc.disable()
+    try:
+        CALLS[call](grads, state)
+        assert len(lib.calls) == 1
+        lib.calls.clear()
+        del grads, state
+        assert not any(r() is not None for r in refs)
+    finally:
+        gc.enable()
+
+
+def test_a_bound_call_keeps_its_tensors(lib):
+    """While the bound call lives, so do the tensors whose addresses it
+    holds."""
+    grads, state = [gpu(100)], [[gpu(100)] for _ in range(4)]
+    refs = [weakref.ref(t) for t in grads + sum(state, [])]
+    mg = ddp.MultiGrad(grads)
+    clip, step = mg.bind_clip(state[3]), mg.bind_adamw(*state[:3])
+    del mg, grads, state
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    clip(1.0)
+    step(1e-3, 1)
+    assert [name for name, _ in lib.calls] == ["grad_clip_multi", "adamw_step_multi"]
