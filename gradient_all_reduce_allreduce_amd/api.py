@@ -334,9 +334,12 @@ def grad_norm_workspace_bytes(numels, ptrs, dtypes):
     """Workspace of grad_norm_multi and grad_clip_multi (host only)."""
     if not len(numels) == len(ptrs) == len(dtypes):
         raise ValueError("numels, ptrs and dtypes must have one entry per tensor")
+    return _norm_bytes((len(numels), _long_array(numels), N.pointer_array(ptrs), _int_array(dtypes)))
+
+
+def _norm_bytes(tensors):
     b = ctypes.c_int64(0)
-    _check(N.lib().grad_norm_workspace_bytes(len(numels), _long_array(numels), N.pointer_array(ptrs),
-                                             _int_array(dtypes), ctypes.byref(b)))
+    _check(N.lib().grad_norm_workspace_bytes(*tensors, ctypes.byref(b)))
     return b.value
 
 
@@ -841,6 +844,30 @@ def _scalar(x, dtype, device, what):
     return x
 
 
+class _Held:
+    """Tensors whose addresses a bound call keeps, and those addresses as the
+    library takes them.  Holding the storages too keeps a held tensor's old
+    memory from anyone else after ``t.data = other`` or ``t.set_()``: an
+    address that is unchanged lies in the same memory."""
+
+    def __init__(self, tensors, what):
+        self.tensors, self._what = tuple(tensors), what
+        self._at = [t.data_ptr() for t in tensors]
+        self._numels = [t.numel() for t in tensors]
+        self._storages = [t.untyped_storage() for t in tensors]
+        self.ptrs = N.pointer_array(self._at)
+
+    def check(self):
+        """Refuses tensors that lie elsewhere, or have another size, than when
+        they were bound: 0.2 us each on the host."""
+        at, numels = [t.data_ptr() for t in self.tensors], [t.numel() for t in self.tensors]
+        if at == self._at and numels == self._numels:
+            return
+        k = next(k for k in range(len(at)) if (at[k], numels[k]) != (self._at[k], self._numels[k]))
+        raise ValueError(f"{self._what}[{k}] has been given other memory or another size since it was bound "
+                         "(t.data = ..., set_, resize_): bind it again")
+
+
 class MultiGrad:
     """Global norm, clipping and the AdamW step of one replica's gradients,
     many tensors per launch.  ``grads``: GPU tensors (or one), contiguous,
@@ -848,8 +875,10 @@ class MultiGrad:
     addresses taken once; every call works on those same tensors, which this
     object keeps alive, and is enqueued on the stream current at the call.
     Gradients that are replaced by new tensors (zero_grad(set_to_none=True))
-    need a new MultiGrad.  Calls may overlap on several streams and be captured
-    into graphs: each takes its own workspace from torch's allocator."""
+    need a new MultiGrad; a held tensor that is given other memory or another
+    size (t.data = ..., set_, resize_) makes every call on it raise ValueError.
+    Calls may overlap on several streams and be captured into graphs: each
+    takes its own workspace from torch's allocator."""
 
     def __init__(self, grads):
         import torch
@@ -857,11 +886,11 @@ class MultiGrad:
         self.device = self.grads[0].device
         self._index = self.device.index
         self._new_norm = functools.partial(torch.empty_like, torch.empty((), dtype=torch.float32, device=self.device))
+        self._held = _Held(self.grads, "grads")
         numels = [g.numel() for g in self.grads]
         codes = [torch_dtype_code(g.dtype) for g in self.grads]
-        ptrs = [g.data_ptr() for g in self.grads]
-        self._list = (len(numels), _long_array(numels), N.pointer_array(ptrs), _int_array(codes))
-        self._bytes = grad_norm_workspace_bytes(numels, ptrs, codes)
+        self._list = (len(numels), _long_array(numels), self._held.ptrs, _int_array(codes))
+        self._bytes = _norm_bytes(self._list)
 
     def _match(self, tensors, what, dtypes):
         """Tensors of the gradients' sizes, one each, on their device."""
@@ -869,16 +898,20 @@ class MultiGrad:
         if len(tensors) != len(self.grads) or tensors[0].device != self.device or \
                 any(x.numel() != g.numel() for x, g in zip(tensors, self.grads)):
             raise ValueError(f"{what}: need one tensor of each gradient's size on its device")
-        return tensors, N.pointer_array([x.data_ptr() for x in tensors])
+        return _Held(tensors, what)
 
     def norm(self):
         """The global 2-norm of all gradients, a float32 scalar tensor."""
+        self._held.check()
+        return self._norm()
+
+    def _norm(self):
         import torch
         # With another GPU current, a launch on the default stream, whose
         # handle names no GPU, would go there.
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
-                return self.norm()
+                return self._norm()
         norm = self._new_norm()
         ws = self._workspace()
         _check(N.lib().grad_norm_multi(*self._list, ws.data_ptr() if ws is not None else None, self._bytes,
@@ -895,32 +928,38 @@ class MultiGrad:
         gradient, of its type; default: in place), and returns the norm:
         the gradients' own, computed in the same call, or the ``norm`` given
         (a float32 scalar tensor, e.g. of ``allreduce_norm``)."""
-        import torch
-        if out is None:
-            out, optrs = self.grads, self._list[2]
-        else:
-            out, optrs = self._match(out, "clip out", (torch.float32, torch.bfloat16))
-            if any(o.dtype != g.dtype for o, g in zip(out, self.grads)):
-                raise ValueError("clip out: every output must have its gradient's type")
+        out = self._outputs(out)
 
         def run(max_norm, norm=None):
-            return self._clip(optrs, max_norm, norm)
+            self._held.check()
+            if out is not self._held:
+                out.check()
+            return self._clip(out, max_norm, norm)
 
-        run.tensors = (self.grads, out)
+        run.tensors = (self.grads, out.tensors)
         return run
 
-    def _clip(self, optrs, max_norm, norm):
+    def _outputs(self, out):
+        import torch
+        if out is None:
+            return self._held
+        out = self._match(out, "clip out", (torch.float32, torch.bfloat16))
+        if any(o.dtype != g.dtype for o, g in zip(out.tensors, self.grads)):
+            raise ValueError("clip out: every output must have its gradient's type")
+        return out
+
+    def _clip(self, out, max_norm, norm):
         import torch
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
-                return self._clip(optrs, max_norm, norm)
+                return self._clip(out, max_norm, norm)
         given, ws = norm is not None, None
         if given:
             _scalar(norm, torch.float32, self.device, "norm")
         else:
             norm = self._new_norm()
             ws = self._workspace()
-        _check(N.lib().grad_clip_multi(*self._list, optrs, max_norm, given, norm.data_ptr(),
+        _check(N.lib().grad_clip_multi(*self._list, out.ptrs, max_norm, given, norm.data_ptr(),
                                        ws.data_ptr() if ws is not None else None, self._bytes,
                                        _raw_stream(self._index)))
         return norm
@@ -936,62 +975,71 @@ class MultiGrad:
         other numbers are taken at the call).  With ``norm`` (a float32 scalar tensor) and ``max_norm`` the gradient is
         clipped on the way, and a norm that is not finite leaves the step
         out.  The gradients must all have one type."""
+        bound = self._state(w, m, v, params)
+
+        def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
+            self._held.check()
+            for x in bound:
+                if x is not None:
+                    x.check()
+            self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm)
+
+        run.tensors = (self.grads, *(x.tensors if x is not None else None for x in bound))
+        return run
+
+    def _state(self, w, m, v, params):
+        """w, m, v and params (or None) as a step takes them."""
         import torch
         if any(g.dtype != self.grads[0].dtype for g in self.grads):
             raise ValueError("adamw: gradients must all have the same element type")
-        gcode = torch_dtype_code(self.grads[0].dtype)
-        w, wptrs = self._match(w, "adamw w", (torch.float32,))
-        m, mptrs = self._match(m, "adamw m", (torch.float32,))
-        v, vptrs = self._match(v, "adamw v", (torch.float32,))
-        pptrs, pcode = None, F32
+        w = self._match(w, "adamw w", (torch.float32,))
+        m = self._match(m, "adamw m", (torch.float32,))
+        v = self._match(v, "adamw v", (torch.float32,))
         if params is not None:
-            params, pptrs = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
-            if any(p.dtype != params[0].dtype for p in params):
+            params = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
+            if any(p.dtype != params.tensors[0].dtype for p in params.tensors):
                 raise ValueError("adamw: params must all have the same element type")
-            pcode = torch_dtype_code(params[0].dtype)
+        return w, m, v, params
 
-        lists = (gcode, wptrs, mptrs, vptrs, pptrs, pcode)
-
-        def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
-            self._adamw(lists, lr, step, betas, eps, weight_decay, norm, max_norm)
-
-        run.tensors = (self.grads, w, m, v, params)
-        return run
-
-    def _adamw(self, lists, lr, step, betas, eps, weight_decay, norm, max_norm):
+    def _adamw(self, bound, lr, step, betas, eps, weight_decay, norm, max_norm):
         import torch
         if (norm is None) != (max_norm is None):
             raise ValueError("adamw: norm and max_norm come together")
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
-                return self._adamw(lists, lr, step, betas, eps, weight_decay, norm, max_norm)
+                return self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm)
         step_dev = norm_dev = None
         if isinstance(step, torch.Tensor):
             step_dev, step = _scalar(step, torch.int64, self.device, "step").data_ptr(), 0
         if norm is not None:
             norm_dev = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
+        w, m, v, params = bound
+        pptrs, pcode = (params.ptrs, torch_dtype_code(params.tensors[0].dtype)) if params is not None else (None, F32)
         count, numels, ptrs, _ = self._list
-        _check(N.lib().adamw_step_multi(count, numels, ptrs, *lists, lr, betas[0], betas[1], eps, weight_decay, step,
+        _check(N.lib().adamw_step_multi(count, numels, ptrs, torch_dtype_code(self.grads[0].dtype), w.ptrs, m.ptrs,
+                                        v.ptrs, pptrs, pcode, lr, betas[0], betas[1], eps, weight_decay, step,
                                         step_dev, norm_dev, max_norm or 0.0, _raw_stream(self._index)))
 
 
 def grad_norm(grads):
     """The global 2-norm of one replica's gradient tensors (float32 scalar
     tensor); see ``MultiGrad``, which a loop over the same tensors keeps."""
-    return MultiGrad(grads).norm()
+    return MultiGrad(grads)._norm()
 
 
 def clip_grads(grads, max_norm, norm=None, out=None):
     """Scale gradient tensors so that their global 2-norm is at most
     ``max_norm``; returns the norm before.  See ``MultiGrad.bind_clip``."""
-    return MultiGrad(grads).bind_clip(out)(max_norm, norm)
+    mg = MultiGrad(grads)
+    return mg._clip(mg._outputs(out), max_norm, norm)
 
 
 def adamw_step(grads, w, m, v, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params=None,
                norm=None, max_norm=None):
     """One AdamW step on lists of tensors (or one flat buffer each); see
     ``MultiGrad.bind_adamw``."""
-    MultiGrad(grads).bind_adamw(w, m, v, params)(lr, step, betas, eps, weight_decay, norm, max_norm)
+    mg = MultiGrad(grads)
+    mg._adamw(mg._state(w, m, v, params), lr, step, betas, eps, weight_decay, norm, max_norm)
 
 
 # The workspace depends on the sizes alone; a training loop asks for the same

@@ -21,7 +21,7 @@ class Gpu(torch.Tensor):
 
 
 def gpu(n, dtype=torch.float32):
-    return torch.zeros(n, dtype=dtype).as_subclass(Gpu)
+    return torch.Tensor._make_subclass(Gpu, torch.zeros(n, dtype=dtype))
 
 
 class Lib:
@@ -87,3 +87,88 @@ def test_a_bound_call_keeps_its_tensors(lib):
     clip(1.0)
     step(1e-3, 1)
     assert [name for name, _ in lib.calls] == ["grad_clip_multi", "adamw_step_multi"]
+
+
+def swap_data(t):
+    t.data = gpu(t.numel(), t.dtype)
+
+
+def swap_storage(t):
+    t.set_(gpu(t.numel(), t.dtype))
+
+
+MOVES = {
+    "data": swap_data,
+    "set": swap_storage,
+    "grown": lambda t: t.resize_(100_000),
+    "shrunk": lambda t: t.resize_(3),
+    "freed": lambda t: t.untyped_storage().resize_(0),
+}
+
+
+@pytest.mark.parametrize("move", MOVES)
+@pytest.mark.parametrize("which", ["grads", "out", "w", "m", "v", "params"])
+def test_a_tensor_given_other_memory_is_refused(lib, which, move):
+    """A held tensor that lies elsewhere, or has another size, than when it
+    was bound: its old address may be anyone's."""
+    t = {k: [gpu(100), gpu(64)] for k in ("grads", "out", "w", "m", "v", "params")}
+    mg = ddp.MultiGrad(t["grads"])
+    clip, step = mg.bind_clip(t["out"]), mg.bind_adamw(t["w"], t["m"], t["v"], t["params"])
+    calls = {"norm": mg.norm, "clip": lambda: clip(1.0), "adamw": lambda: step(1e-3, 1)}
+    reads = {"grads": ("norm", "clip", "adamw"), "out": ("clip",)}.get(which, ("adamw",))
+    for call in calls.values():
+        call()
+    lib.calls.clear()
+    MOVES[move](t[which][1])
+    for name, call in calls.items():
+        if name in reads:
+            with pytest.raises(ValueError, match=rf"{which}\[1\]"):
+                call()
+        else:
+            call()
+    assert len(lib.calls) == 3 - len(reads)
+
+
+def test_in_place_clip_of_a_tensor_given_other_memory(lib):
+    grads = [gpu(100), gpu(64)]
+    clip = ddp.MultiGrad(grads).bind_clip()
+    swap_data(grads[0])
+    with pytest.raises(ValueError, match=r"grads\[0\]"):
+        clip(1.0)
+    assert not lib.calls
+
+
+def test_values_and_flags_may_change(lib):
+    """What moves no memory is no reason to refuse."""
+    g = gpu(100)
+    mg = ddp.MultiGrad([g])
+    g.fill_(3.0)
+    g.requires_grad_(True)
+    mg.norm()
+    mg.bind_clip()(1.0)
+    assert len(lib.calls) == 2
+
+
+def test_memory_is_held_with_its_tensor(lib):
+    """The memory that a bound tensor was taken away from is not handed to
+    another while the handle holds its address."""
+    from torch.multiprocessing.reductions import StorageWeakRef
+    g, out = gpu(100), gpu(100)
+    old = [StorageWeakRef(t.untyped_storage()) for t in (g, out)]
+    mg = ddp.MultiGrad([g])
+    clip = mg.bind_clip([out])
+    swap_data(g)
+    swap_data(out)
+    assert not any(s.expired() for s in old)
+    del mg, clip
+    assert all(s.expired() for s in old)
+
+
+def test_tensors_without_elements_are_held_too(lib):
+    g = [gpu(0), gpu(5)]
+    mg = ddp.MultiGrad(g)
+    mg.norm()
+    g[0].resize_(8)
+    with pytest.raises(ValueError, match=r"grads\[0\]"):
+        mg.norm()
+    assert len(lib.calls) == 1
