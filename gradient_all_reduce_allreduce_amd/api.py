@@ -823,6 +823,9 @@ def _tensor_list(tensors, what, dtypes):
     tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
     if not tensors:
         raise ValueError(f"{what}: need at least one tensor")
+    for t in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: {type(t).__name__} where a tensor is needed")
     device = tensors[0].device
     for t in tensors:
         if not t.is_cuda:
@@ -1021,15 +1024,35 @@ class MultiGrad:
                                         step_dev, norm_dev, max_norm or 0.0, _raw_stream(self._index)))
 
 
+def _present(grads, out=None):
+    """The gradients that are not None (a parameter that is frozen or took
+    no part has none), and their entries of ``out``."""
+    import torch
+    if isinstance(grads, torch.Tensor):
+        return grads, out
+    grads = list(grads)
+    if all(g is not None for g in grads):
+        return grads, out
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(out) != len(grads):
+            raise ValueError("clip out: need one entry per gradient")
+        out = [o for g, o in zip(grads, out) if g is not None]
+    return [g for g in grads if g is not None], out
+
+
 def grad_norm(grads):
     """The global 2-norm of one replica's gradient tensors (float32 scalar
-    tensor); see ``MultiGrad``, which a loop over the same tensors keeps."""
-    return MultiGrad(grads)._norm()
+    tensor), entries that are None left out; see ``MultiGrad``, which a loop
+    over the same tensors keeps."""
+    return MultiGrad(_present(grads)[0])._norm()
 
 
 def clip_grads(grads, max_norm, norm=None, out=None):
     """Scale gradient tensors so that their global 2-norm is at most
-    ``max_norm``; returns the norm before.  See ``MultiGrad.bind_clip``."""
+    ``max_norm``; returns the norm before.  Entries that are None are left
+    out, ``out`` not looked at in their places.  See ``MultiGrad.bind_clip``."""
+    grads, out = _present(grads, out)
     mg = MultiGrad(grads)
     return mg._clip(mg._outputs(out), max_norm, norm)
 

@@ -172,3 +172,41 @@ def test_tensors_without_elements_are_held_too(lib):
     with pytest.raises(ValueError, match=r"grads\[0\]"):
         mg.norm()
     assert len(lib.calls) == 1
+
+
+def addresses(array, count):
+    return [array[k] for k in range(count)]
+
+
+def test_parameters_without_a_gradient_are_skipped(lib):
+    """grad_norm and clip_grads of [p.grad for p in model.parameters()], where
+    a frozen or unused parameter's is None."""
+    a, b = gpu(100), gpu(7)
+    ddp.grad_norm([None, a, None, b])
+    ddp.clip_grads((x for x in (a, None, b)), 1.0)
+    x, y = gpu(100), gpu(7)
+    ddp.clip_grads([a, None, b], 1.0, out=[x, None, y])
+    ddp.clip_grads([a, None, b], 1.0, out=[x, gpu(9), y])       # the place of a skipped one
+    want = [a.data_ptr(), b.data_ptr()]
+    outs = [want] + 2 * [[x.data_ptr(), y.data_ptr()]]
+    assert [name for name, _ in lib.calls] == ["grad_norm_multi"] + 3 * ["grad_clip_multi"]
+    for k, (_, args) in enumerate(lib.calls):
+        assert args[0] == 2 and addresses(args[1], 2) == [100, 7] and addresses(args[2], 2) == want
+        if k:
+            assert addresses(args[4], 2) == outs[k - 1]
+
+
+def test_skipping_refusals(lib):
+    a = gpu(5)
+    for call in (lambda: ddp.grad_norm([None]), lambda: ddp.clip_grads([None, None], 1.0),
+                 lambda: ddp.clip_grads([a, None], 1.0, out=[gpu(5)]),
+                 lambda: ddp.clip_grads([a, None], 1.0, out=[None, gpu(5)])):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    # one tensor per entry where every entry has a state of its own
+    for call in (lambda: ddp.MultiGrad([a, None]), lambda: ddp.MultiGrad([None, a]),
+                 lambda: ddp.adamw_step([a, None], [a, a], [a, a], [a, a], 1e-3, 1),
+                 lambda: ddp.adamw_step([a], [None], [a], [a], 1e-3, 1), lambda: ddp.grad_norm([a, 3.0])):
+        with pytest.raises(TypeError, match="tensor"):
+            call()
+    assert not lib.calls
