@@ -451,10 +451,9 @@ def _rank_tensors(tensors, what):
     t0 = tensors[0]
     device, dtype, numel = t0.get_device(), t0.dtype, t0.numel()
     for t in tensors:
-        d = t.get_device()
-        if d < 0:
+        if not t.is_cuda:
             raise ValueError(f"{what}: tensors must live on the GPU")
-        if d != device or t.dtype != dtype or t.numel() != numel:
+        if t.get_device() != device or t.dtype != dtype or t.numel() != numel:
             raise ValueError(f"{what}: every rank needs the same device, dtype and size")
         if not t.is_contiguous():
             raise ValueError(f"{what}: tensors must be contiguous")
