@@ -847,27 +847,35 @@ def _scalar(x, dtype, device, what):
 
 
 class _Held:
-    """Tensors whose addresses a bound call keeps, and those addresses as the
-    library takes them.  Holding the storages too keeps a held tensor's old
-    memory from anyone else after ``t.data = other`` or ``t.set_()``: an
-    address that is unchanged lies in the same memory."""
+    """Tensors of a call, and their addresses as the library takes them."""
 
-    def __init__(self, tensors, what):
-        self.tensors, self._what = tuple(tensors), what
-        self._at = [t.data_ptr() for t in tensors]
-        self._numels = [t.numel() for t in tensors]
-        self._storages = [t.untyped_storage() for t in tensors]
-        self.ptrs = N.pointer_array(self._at)
+    def __init__(self, tensors, what, numels):
+        self.tensors, self.what, self.numels = tuple(tensors), what, numels
+        self.at = [t.data_ptr() for t in tensors]
+        self.ptrs = N.pointer_array(self.at)
 
-    def check(self):
-        """Refuses tensors that lie elsewhere, or have another size, than when
-        they were bound: 0.2 us each on the host."""
-        at, numels = [t.data_ptr() for t in self.tensors], [t.numel() for t in self.tensors]
-        if at == self._at and numels == self._numels:
+
+def _unmoved(*held):
+    """Returns ``check()``, which refuses held tensors that lie elsewhere, or
+    have another size, than when they were bound (0.07 us each on the host).
+    It holds their storages, which keeps a held tensor's old memory from anyone
+    else after ``t.data = other`` or ``t.set_()``: an address that is unchanged
+    lies in the same memory."""
+    import torch
+    data_ptr, numel = torch.Tensor.data_ptr, torch.Tensor.numel
+    tensors = sum((h.tensors for h in held), ())
+    at, numels = sum((h.at for h in held), []), sum((h.numels for h in held), [])
+
+    def check():
+        if list(map(data_ptr, tensors)) == at and list(map(numel, tensors)) == numels:
             return
-        k = next(k for k in range(len(at)) if (at[k], numels[k]) != (self._at[k], self._numels[k]))
-        raise ValueError(f"{self._what}[{k}] has been given other memory or another size since it was bound "
-                         "(t.data = ..., set_, resize_): bind it again")
+        for h in held:
+            for k, t in enumerate(h.tensors):
+                if t.data_ptr() != h.at[k] or t.numel() != h.numels[k]:
+                    raise ValueError(f"{h.what}[{k}] has been given other memory or another size since it was bound "
+                                     "(t.data = ..., set_, resize_): bind it again")
+    check.storages = [t.untyped_storage() for t in tensors]
+    return check
 
 
 class MultiGrad:
@@ -888,23 +896,23 @@ class MultiGrad:
         self.device = self.grads[0].device
         self._index = self.device.index
         self._new_norm = functools.partial(torch.empty_like, torch.empty((), dtype=torch.float32, device=self.device))
-        self._held = _Held(self.grads, "grads")
-        numels = [g.numel() for g in self.grads]
+        self._held = _Held(self.grads, "grads", [g.numel() for g in self.grads])
+        self._check = _unmoved(self._held)
         codes = [torch_dtype_code(g.dtype) for g in self.grads]
-        self._list = (len(numels), _long_array(numels), self._held.ptrs, _int_array(codes))
+        self._list = (len(codes), _long_array(self._held.numels), self._held.ptrs, _int_array(codes))
         self._bytes = _norm_bytes(self._list)
 
     def _match(self, tensors, what, dtypes):
         """Tensors of the gradients' sizes, one each, on their device."""
         tensors = _tensor_list(tensors, what, dtypes)
-        if len(tensors) != len(self.grads) or tensors[0].device != self.device or \
-                any(x.numel() != g.numel() for x, g in zip(tensors, self.grads)):
+        numels = [x.numel() for x in tensors]
+        if numels != self._held.numels or tensors[0].device != self.device:
             raise ValueError(f"{what}: need one tensor of each gradient's size on its device")
-        return _Held(tensors, what)
+        return _Held(tensors, what, numels)
 
     def norm(self):
         """The global 2-norm of all gradients, a float32 scalar tensor."""
-        self._held.check()
+        self._check()
         return self._norm()
 
     def _norm(self):
@@ -931,11 +939,10 @@ class MultiGrad:
         the gradients' own, computed in the same call, or the ``norm`` given
         (a float32 scalar tensor, e.g. of ``allreduce_norm``)."""
         out = self._outputs(out)
+        check = self._check if out is self._held else _unmoved(self._held, out)
 
         def run(max_norm, norm=None):
-            self._held.check()
-            if out is not self._held:
-                out.check()
+            check()
             return self._clip(out, max_norm, norm)
 
         run.tensors = (self.grads, out.tensors)
@@ -978,12 +985,10 @@ class MultiGrad:
         clipped on the way, and a norm that is not finite leaves the step
         out.  The gradients must all have one type."""
         bound = self._state(w, m, v, params)
+        check = _unmoved(self._held, *(x for x in bound if x is not None))
 
         def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
-            self._held.check()
-            for x in bound:
-                if x is not None:
-                    x.check()
+            check()
             self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm)
 
         run.tensors = (self.grads, *(x.tensors if x is not None else None for x in bound))
