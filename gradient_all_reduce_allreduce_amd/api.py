@@ -888,7 +888,10 @@ class MultiGrad:
     need a new MultiGrad; a held tensor that is given other memory or another
     size (t.data = ..., set_, resize_) makes every call on it raise ValueError.
     Calls may overlap on several streams and be captured into graphs: each
-    takes its own workspace from torch's allocator."""
+    takes its own workspace from torch's allocator.  What a call writes
+    (clipped gradients, w, m, v, params) it writes past autograd, as every call
+    of this package does: no version counter moves, so nothing that a backward
+    pass still to come has saved may be among it."""
 
     def __init__(self, grads):
         import torch
@@ -981,9 +984,10 @@ class MultiGrad:
         ``params`` (float32 or bfloat16) if given.  ``step``: the step's
         number from 1, an int or a tensor of one int64 on the GPU (read when
         the step runs, so that a captured step can be replayed; ``lr`` and the
-        other numbers are taken at the call).  With ``norm`` (a float32 scalar tensor) and ``max_norm`` the gradient is
-        clipped on the way, and a norm that is not finite leaves the step
-        out.  The gradients must all have one type."""
+        other numbers are taken at the call, so that a captured step keeps
+        them).  With ``norm`` (a float32 scalar tensor) and ``max_norm`` the
+        gradient is clipped on the way, and a norm that is not finite leaves
+        the step out.  The gradients must all have one type."""
         bound = self._state(w, m, v, params)
         check = _unmoved(self._held, *(x for x in bound if x is not None))
 

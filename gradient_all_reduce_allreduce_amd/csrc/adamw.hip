@@ -31,7 +31,7 @@
 // batch of scalar loads; what the step needs besides (the norm, the step's
 // number, divisions, two powers) is worked out while the data is in flight.
 // (The norm and the count read as vector loads waited for the tile's data first:
-// 463 us with the count on the GPU, 378 now.)  Addresses and sizes travel in
+// 463 us with the count on the GPU, 372 now.)  Addresses and sizes travel in
 // the kernel arguments, several launches for more tensors than fit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -24,21 +24,21 @@
 // set larger than the caches is read twice.  What carries each kernel:
 //   * the norm: 1,024 workgroups of 256 lanes take every 1,024th tile of 16
 //     KiB, four non-temporal 16-byte loads a lane in flight.  2.0B bf16
-//     elements 580 us, 7.0 TB/s; 86.6M 29 us.  With ordinary loads 6.0 TB/s; a
-//     contiguous run of tiles per workgroup 7% slower; 2,048 workgroups 4%.
-//     2,048 one-wave workgroups reach 7.2 TB/s on the 2.0B elements, but lose
-//     5% on 86.6M and 3% on ragged sets.
+//     elements 590 us with the partials' sum, 6.85 TB/s; 86.6M 29 us.  With
+//     ordinary loads 6.0 TB/s; a contiguous run of tiles per workgroup 7% slower;
+//     2,048 workgroups 4%.  2,048 one-wave workgroups are 3% faster on the 2.0B
+//     elements, but lose 5% on 86.6M and 3% on ragged sets.
 //   * the scaling: one one-wave workgroup per 4 KiB tile, 12 of them on a CU.
 //     300M float32 370 us, 6.5 TB/s; 2,048 workgroups of 256 walking over the
-//     tiles 5.1 TB/s, two tiles a workgroup 6.3.  In place with c = 1 it has
-//     nothing to do but start: 63 us.  It begins with the last tile.
-//     (Reading the end of the set for the norm with loads meant to stay in
-//     cache changed nothing.)
+//     tiles 5.1 TB/s, two tiles a workgroup 6.3.  In place with c = 1 all of
+//     them start only to end, 63 us for 300M and 106 for 507M, where one read
+//     of the norm is needed: not looked into yet, as it may cost c < 1 some
+//     of its rate.
 //   * few small tensors: one launch of one workgroup for norm and scaling.
-//     24 tensors of 1,000 float32: norm 2.7 us on the GPU and 6.1 a call against
-//     4.0 and 9.2 for the wide kernels, clip 3.9 and 6.6 against 7.6 and 13.3;
-//     at the limit of 64 tiles level on the GPU (clip 7.0 against 6.1 us), a
-//     third less per call.
+//     24 tensors of 1,000 float32: norm 2.7 us on the GPU against 4.0 for the
+//     wide kernels and 3.1 less per call on the host, clip 3.9 against 7.6 and
+//     6.7 less per call; at the limit of 64 tiles level on the GPU (clip 7.0
+//     against 6.1 us), and still less per call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -317,7 +317,9 @@ __global__ __launch_bounds__(kClipBlock) void clip_kernel(ClipArgs) {
     const float c = gv::clip_factor(gv::load_uniform(a->norm), a->max_norm);
     if (a->in_place && c == 1.0f) return;   // what is there is the result
     const uint32_t tiles = a->tiles;
-    // From the last tile back: what was read last is likeliest in cache.
+    // From the last tile back.  (From the first on measures the same within 1%:
+    // 300M float32 368 us back, 366 on; 507M 621 and 621; 86.6M bf16 after their
+    // own norm 86 and 86.)
     for (uint32_t back = blockIdx.x; back < tiles; back += gridDim.x) {
         const uint32_t tile = tiles - 1 - back;
         const int t = piece_at(a, tile);

@@ -9,7 +9,7 @@
 // writes one partial; a second, small launch adds the partials
 // (grad_norm.hip).  The squares and the wave's sum cost nothing that shows: at
 // P = 8, 25.6M float32, all ranks written, 251 us without the second launch
-// against 248 for the plain all-reduce, and 255 (6.4 TB/s) with it.  86.6M bf16
+// against 248 for the plain all-reduce, and 257 (6.4 TB/s) with it.  86.6M bf16
 // into one float32 copy 268 us, 6.5 TB/s (the plain call writes 8 copies).
 #include "grad_vec.h"
 #include "ring_norm.h"

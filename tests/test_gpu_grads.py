@@ -15,6 +15,9 @@ pytestmark = pytest.mark.gpu
 ddp = pytest.importorskip("gradient_all_reduce_allreduce_amd")
 
 TILE = 16384                      # bytes of one norm or clip tile
+# (The norm's, for sets past 64 pieces of 4 KiB: of these "many" and "long".  The
+# clip's is 4 KiB, AdamW's 256 elements.  test_gpu_grads_paths.py has the ends of
+# the tiles on every path.)
 SIZES = {
     "one": [1],
     "few": [5, 1, 0, 33, 4097],
