@@ -21,7 +21,10 @@ from .api import (SUM, MEAN, F32, BF16, MAX_RANKS, DdpError, ddp_bucket_plan, dd
                   allreduce_ring_stepwise_buckets, allreduce_hierarchical_buckets,
                   NORM_WORKSPACE_BYTES, grad_norm_multi, grad_norm_workspace_bytes, grad_clip_multi, allreduce_ring_norm,
                   allreduce_ring_norm_buckets, allreduce_norm_workspace_bytes, adamw_step_multi,
-                  MultiGrad, grad_norm, clip_grads, adamw_step, allreduce_norm)
+                  MultiGrad, grad_norm, clip_grads, adamw_step, allreduce_norm,
+                  MX_BLOCK, mx4_quantize_rows, mx4_dequantize_rows, allreduce_mx4_rows, allreduce_mx4_coded,
+                  allreduce_mx4_workspace_bytes, adamw8_step_multi, adamw8_read_multi, Moments8, adamw8_step)
+from .mx4 import Mx4, mx4_quantize, mx4_dequantize, allreduce_mx4, allreduce_mx4_norm
 from .bucketer import GradBucketer
 
 __all__ = [
@@ -41,4 +44,7 @@ __all__ = [
     "NORM_WORKSPACE_BYTES", "grad_norm_multi", "grad_norm_workspace_bytes", "grad_clip_multi", "allreduce_ring_norm",
     "allreduce_ring_norm_buckets", "allreduce_norm_workspace_bytes", "adamw_step_multi",
     "MultiGrad", "grad_norm", "clip_grads", "adamw_step", "allreduce_norm",
+    "MX_BLOCK", "mx4_quantize_rows", "mx4_dequantize_rows", "allreduce_mx4_rows", "allreduce_mx4_coded",
+    "allreduce_mx4_workspace_bytes", "adamw8_step_multi", "adamw8_read_multi", "Moments8", "adamw8_step",
+    "Mx4", "mx4_quantize", "mx4_dequantize", "allreduce_mx4", "allreduce_mx4_norm",
 ]

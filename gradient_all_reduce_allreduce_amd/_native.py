@@ -30,6 +30,7 @@ DDP_F32 = 0
 DDP_BF16 = 1
 DDP_MAX_RANKS = 16
 DDP_NORM_WORKSPACE_BYTES = 1 << 13
+DDP_MX_BLOCK = 32
 
 # ddp_kernel_family
 KERNEL_FAMILIES = {"ring": 0, "ring_sgd": 1, "tree": 2, "reduce_scatter": 3, "all_gather": 4,
@@ -161,6 +162,29 @@ _SIGNATURES = {
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_double,
         ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_int64,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_double, ctypes.c_void_p]),
+    "mx4_quantize": (ctypes.c_int, [
+        ctypes.c_int32, _c_void_pp, ctypes.c_int, ctypes.c_int64, _c_void_pp, ctypes.c_int,
+        _c_void_pp, _c_void_pp, ctypes.c_void_p]),
+    "mx4_dequantize": (ctypes.c_int, [
+        ctypes.c_int32, _c_void_pp, _c_void_pp, ctypes.c_int64, _c_void_pp, ctypes.c_int,
+        ctypes.c_void_p]),
+    "allreduce_mx4": (ctypes.c_int, [
+        ctypes.c_int, ctypes.c_int32, _c_void_pp, _c_void_pp, ctypes.c_int64, ctypes.c_int32,
+        _c_void_pp, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "allreduce_mx4_coded": (ctypes.c_int, [
+        ctypes.c_int, ctypes.c_int32, _c_void_pp, _c_void_pp, ctypes.c_int64, ctypes.c_int32,
+        _c_void_pp, _c_void_pp, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_int64, ctypes.c_void_p]),
+    "allreduce_mx4_workspace_bytes": (ctypes.c_int, [ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
+    "adamw8_step_multi": (ctypes.c_int, [
+        ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+        ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+        ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double,
+        ctypes.c_void_p]),
+    "adamw8_read_multi": (ctypes.c_int, [
+        ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "ddp_set_wg_per_cu": (ctypes.c_int, [ctypes.c_int, ctypes.c_int32]),
     "ddp_last_error": (ctypes.c_char_p, []),
 }

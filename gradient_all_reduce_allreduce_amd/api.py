@@ -14,7 +14,11 @@ Python ints, stream as an int handle or None):
     allreduce_hierarchical_emulated, ddp_multi_plan, ddp_multi_block_map, allreduce_multi_ring_emulated,
     allreduce_multi_fused_sgd, allreduce_multi_ring_noalloc, grad_norm_multi, grad_clip_multi,
     allreduce_ring_norm, allreduce_ring_norm_buckets, allreduce_norm_workspace_bytes,
-    adamw_step_multi, grad_norm_workspace_bytes, ddp_set_wg_per_cu
+    adamw_step_multi, grad_norm_workspace_bytes, mx4_quantize_rows, mx4_dequantize_rows,
+    allreduce_mx4_rows, allreduce_mx4_coded, allreduce_mx4_workspace_bytes, adamw8_step_multi,
+    adamw8_read_multi, ddp_set_wg_per_cu
+(mx4_quantize, mx4_dequantize and allreduce_mx4 of the C header end in _rows here: the tensor-level helpers have the
+short names.)
 Tensor-level helpers:
     allreduce(tensors, op, chunking, out)            -> list of outputs
     allreduce_sgd(grads, w, v, lr, mu, op, chunking, out)
@@ -24,6 +28,9 @@ Tensor-level helpers:
     allreduce_norm(tensors, op, chunking, out)       -> (outputs, norm)
     grad_norm(grads), clip_grads(grads, max_norm), adamw_step(grads, w, m, v, lr, step),
     MultiGrad(grads)
+    mx4_quantize(tensors, residual), mx4_dequantize(coded), allreduce_mx4(coded, op, out),
+    allreduce_mx4_norm(coded, op, out)               -> (outputs, norm); see mx4.py
+    adamw8_step(grads, w, moments, lr, step), Moments8
 """
 
 import ctypes
@@ -39,6 +46,7 @@ F32 = N.DDP_F32
 BF16 = N.DDP_BF16
 MAX_RANKS = N.DDP_MAX_RANKS
 NORM_WORKSPACE_BYTES = N.DDP_NORM_WORKSPACE_BYTES
+MX_BLOCK = N.DDP_MX_BLOCK
 
 
 class DdpError(RuntimeError):
@@ -390,6 +398,67 @@ def adamw_step_multi(numels, grads, grad_dtype, w, m, v, params, param_dtype, lr
                                     N.pointer_array(params) if params is not None else None, param_dtype,
                                     lr, beta1, beta2, eps, weight_decay, step, step_dev, norm, max_norm,
                                     stream))
+
+
+def _ptrs_or_none(ptrs):
+    return _ptr_array(ptrs) if ptrs is not None else None
+
+
+def mx4_quantize_rows(P, rank_in, in_dtype, n, rank_residual, residual_dtype, rank_codes, rank_scales, stream=None):
+    """``rank_residual``: P addresses or None."""
+    _check(N.lib().mx4_quantize(P, _ptrs_or_none(rank_in), in_dtype, n, _ptrs_or_none(rank_residual), residual_dtype,
+                                _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), stream))
+
+
+def mx4_dequantize_rows(P, rank_codes, rank_scales, n, rank_out, out_dtype, stream=None):
+    _check(N.lib().mx4_dequantize(P, _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), n,
+                                  _ptrs_or_none(rank_out), out_dtype, stream))
+
+
+def allreduce_mx4_rows(op, P, rank_codes, rank_scales, n, rank_out, out_dtype, norm=None, workspace=None,
+                       workspace_bytes=0, stream=None):
+    """``rank_out``: P addresses, or one (a single copy of the result)."""
+    _check(N.lib().allreduce_mx4(_op(op), P, _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), n, len(rank_out),
+                                 _ptrs_or_none(rank_out), out_dtype, norm, workspace, workspace_bytes, stream))
+
+
+def allreduce_mx4_coded(op, P, rank_codes, rank_scales, n, out_codes, out_scales, residual=None, residual_dtype=F32,
+                        norm=None, workspace=None, workspace_bytes=0, stream=None):
+    """``out_codes``, ``out_scales``: P addresses each, or one."""
+    if len(out_codes) != len(out_scales):
+        raise ValueError("out_codes and out_scales must have one entry per row")
+    _check(N.lib().allreduce_mx4_coded(_op(op), P, _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), n,
+                                       len(out_codes), _ptrs_or_none(out_codes), _ptrs_or_none(out_scales), residual,
+                                       residual_dtype, norm, workspace, workspace_bytes, stream))
+
+
+def allreduce_mx4_workspace_bytes(n):
+    """Workspace of the two calls above with a norm (host only)."""
+    b = ctypes.c_int64(0)
+    _check(N.lib().allreduce_mx4_workspace_bytes(n, ctypes.byref(b)))
+    return b.value
+
+
+def adamw8_step_multi(numels, grads, grad_dtype, w, m, v, scales, params, param_dtype, lr, beta1, beta2, eps,
+                      weight_decay, step, step_dev=None, seed=0, norm=None, max_norm=0.0, stream=None):
+    """adamw_step_multi with 8-bit moments: ``m``, ``v``, ``scales`` are host
+    lists of device addresses too."""
+    for x in (grads, w, m, v, scales) + ((params,) if params is not None else ()):
+        if len(x) != len(numels):
+            raise ValueError("every list must have one entry per tensor")
+    _check(N.lib().adamw8_step_multi(len(numels), _long_array(numels), N.pointer_array(grads), grad_dtype,
+                                     N.pointer_array(w), N.pointer_array(m), N.pointer_array(v),
+                                     N.pointer_array(scales), _ptrs_or_none(params), param_dtype, lr, beta1, beta2,
+                                     eps, weight_decay, step, step_dev, seed, norm, max_norm, stream))
+
+
+def adamw8_read_multi(numels, m, v, scales, m_out, v_out, out_dtype, stream=None):
+    for x in (m, v, scales, m_out, v_out):
+        if len(x) != len(numels):
+            raise ValueError("every list must have one entry per tensor")
+    _check(N.lib().adamw8_read_multi(len(numels), _long_array(numels), N.pointer_array(m), N.pointer_array(v),
+                                     N.pointer_array(scales), N.pointer_array(m_out), N.pointer_array(v_out),
+                                     out_dtype, stream))
 
 
 def ddp_set_wg_per_cu(family, wg_per_cu):
@@ -1004,32 +1073,67 @@ class MultiGrad:
         if any(g.dtype != self.grads[0].dtype for g in self.grads):
             raise ValueError("adamw: gradients must all have the same element type")
         w = self._match(w, "adamw w", (torch.float32,))
-        m = self._match(m, "adamw m", (torch.float32,))
-        v = self._match(v, "adamw v", (torch.float32,))
+        m = self._match(m, "adamw m", (torch.float32,)) if m is not None else None
+        v = self._match(v, "adamw v", (torch.float32,)) if v is not None else None
         if params is not None:
             params = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
             if any(p.dtype != params.tensors[0].dtype for p in params.tensors):
                 raise ValueError("adamw: params must all have the same element type")
         return w, m, v, params
 
-    def _adamw(self, bound, lr, step, betas, eps, weight_decay, norm, max_norm):
+    def bind_adamw8(self, w, moments, params=None):
+        """``bind_adamw`` with the moments in 8 bits: ``moments`` is a
+        ``Moments8`` of tensors of the gradients' sizes.  Returns ``run(lr, step,
+        betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None,
+        max_norm=None, seed=0)``.  The moments are rounded at random, by a hash
+        of ``seed``, ``step`` and each element's place: the same call gives the
+        same bits, and replicas that are to stay identical need the same
+        seed."""
+        bound = self._state8(w, moments, params)
+        check = _unmoved(self._held, *(x for x in bound if x is not None))
+
+        def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None, seed=0):
+            check()
+            self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm, seed)
+
+        run.tensors = (self.grads, *(x.tensors if x is not None else None for x in bound))
+        return run
+
+    def _state8(self, w, moments, params):
+        """w, m, v, scales and params (or None) as a step takes them."""
+        import torch
+        if not isinstance(moments, Moments8):
+            raise TypeError(f"adamw8: moments must be a Moments8, not {type(moments).__name__}")
+        m, v, scales = moments._held
+        if m.numels != self._held.numels or moments.device != self.device:
+            raise ValueError("adamw8: need moments of each gradient's size on its device")
+        moments._check()
+        w, _, _, params = self._state(w, None, None, params)
+        return w, m, v, scales, params
+
+    def _adamw(self, bound, lr, step, betas, eps, weight_decay, norm, max_norm, seed=None):
+        """``seed``: of a step with 8-bit moments, else None."""
         import torch
         if (norm is None) != (max_norm is None):
             raise ValueError("adamw: norm and max_norm come together")
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
-                return self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm)
+                return self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm, seed)
         step_dev = norm_dev = None
         if isinstance(step, torch.Tensor):
             step_dev, step = _scalar(step, torch.int64, self.device, "step").data_ptr(), 0
         if norm is not None:
             norm_dev = _scalar(norm, torch.float32, self.device, "norm").data_ptr()
-        w, m, v, params = bound
+        *state, params = bound
         pptrs, pcode = (params.ptrs, torch_dtype_code(params.tensors[0].dtype)) if params is not None else (None, F32)
         count, numels, ptrs, _ = self._list
-        _check(N.lib().adamw_step_multi(count, numels, ptrs, torch_dtype_code(self.grads[0].dtype), w.ptrs, m.ptrs,
-                                        v.ptrs, pptrs, pcode, lr, betas[0], betas[1], eps, weight_decay, step,
-                                        step_dev, norm_dev, max_norm or 0.0, _raw_stream(self._index)))
+        args = [count, numels, ptrs, torch_dtype_code(self.grads[0].dtype), *(x.ptrs for x in state), pptrs, pcode, lr,
+                betas[0], betas[1], eps, weight_decay, step, step_dev]
+        end = (norm_dev, max_norm or 0.0, _raw_stream(self._index))
+        if seed is None:
+            _check(N.lib().adamw_step_multi(*args, *end))
+        else:
+            _check(N.lib().adamw8_step_multi(*args, seed, *end))
 
 
 def _present(grads, out=None):
@@ -1071,6 +1175,101 @@ def adamw_step(grads, w, m, v, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_de
     ``MultiGrad.bind_adamw``."""
     mg = MultiGrad(grads)
     mg._adamw(mg._state(w, m, v, params), lr, step, betas, eps, weight_decay, norm, max_norm)
+
+
+class Moments8:
+    """The two moments of AdamW in 8 bits: for each tensor ``m`` and ``v``, a
+    byte per element, and ``scales``, two bytes per block of 32 elements (lists
+    of contiguous uint8 GPU tensors; adamw8_step_multi in the C header has the
+    formats).  They are what a checkpoint keeps; ``Moments8(m, v, scales)``
+    makes them usable again, and ``Moments8.zeros`` new ones.  The tensors are
+    checked and their addresses taken once, and a tensor that is given other
+    memory or another size afterwards is refused."""
+
+    def __init__(self, m, v, scales):
+        import torch
+        held = []
+        for x, what in ((m, "m"), (v, "v"), (scales, "scales")):
+            x = _tensor_list(x, f"Moments8 {what}", (torch.uint8,))
+            held.append(_Held(x, f"Moments8 {what}", [t.numel() for t in x]))
+        numels = held[0].numels
+        if held[1].numels != numels or held[2].numels != [2 * (-(-n // MX_BLOCK)) for n in numels]:
+            raise ValueError("Moments8: need a byte of m and of v per element and two scale bytes per block of 32")
+        self.m, self.v, self.scales = (list(h.tensors) for h in held)
+        self.device = self.m[0].device
+        if any(h.tensors[0].device != self.device for h in held):
+            raise ValueError("Moments8: every tensor must live on the same GPU")
+        self._held = held
+        self._check = _unmoved(*held)
+
+    @classmethod
+    def zeros(cls, tensors):
+        """Moments before the first step, of the sizes of ``tensors`` (or one),
+        on their device, in one allocation, each on a 128-byte line."""
+        import torch
+        tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+        if not tensors:
+            raise ValueError("Moments8.zeros: need at least one tensor")
+        numels = [t.numel() for t in tensors]
+        sizes = numels + numels + [2 * (-(-n // MX_BLOCK)) for n in numels]
+        padded = [-(-n // 128) * 128 for n in sizes]
+        parts = torch.zeros(sum(padded), dtype=torch.uint8, device=tensors[0].device).split(padded)
+        parts = [p[:n] for p, n in zip(parts, sizes)]
+        T = len(tensors)
+        return cls(parts[:T], parts[T:2 * T], parts[2 * T:])
+
+    def bind_read(self, m_out, v_out):
+        """Returns ``run()``, which writes the moments' values to ``m_out`` and
+        ``v_out`` (one tensor of each size, all float32 or all bfloat16)."""
+        bound = self._outputs(m_out, v_out)
+        check = _unmoved(*self._held, *bound)
+
+        def run():
+            check()
+            self._read(bound)
+
+        run.tensors = (self.m, self.v, self.scales, *(x.tensors for x in bound))
+        return run
+
+    def _outputs(self, m_out, v_out):
+        import torch
+        bound = []
+        for x, what in ((m_out, "m_out"), (v_out, "v_out")):
+            x = _tensor_list(x, f"Moments8 {what}", (torch.float32, torch.bfloat16))
+            if [t.numel() for t in x] != self._held[0].numels or x[0].device != self.device:
+                raise ValueError(f"Moments8 {what}: need one tensor of each moment's size on its device")
+            bound.append(_Held(x, f"Moments8 {what}", self._held[0].numels))
+        if len({t.dtype for h in bound for t in h.tensors}) > 1:
+            raise ValueError("Moments8: outputs must all have the same element type")
+        return bound
+
+    def read(self, dtype=None):
+        """The moments' values as new tensors (default float32): (list of m,
+        list of v)."""
+        import torch
+        self._check()
+        m, v = ([torch.empty(n, dtype=dtype or torch.float32, device=self.device) for n in self._held[0].numels]
+                for _ in range(2))
+        self._read(self._outputs(m, v))
+        return m, v
+
+    def _read(self, bound):
+        import torch
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device.index):
+                return self._read(bound)
+        m, v, scales = self._held
+        _check(N.lib().adamw8_read_multi(len(m.numels), _long_array(m.numels), m.ptrs, v.ptrs, scales.ptrs,
+                                         bound[0].ptrs, bound[1].ptrs, torch_dtype_code(bound[0].tensors[0].dtype),
+                                         _raw_stream(self.device.index)))
+
+
+def adamw8_step(grads, w, moments, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params=None, norm=None,
+                max_norm=None, seed=0):
+    """``adamw_step`` with the moments in 8 bits (a ``Moments8``); see
+    ``MultiGrad.bind_adamw8``."""
+    mg = MultiGrad(grads)
+    mg._adamw(mg._state8(w, moments, params), lr, step, betas, eps, weight_decay, norm, max_norm, seed)
 
 
 # The workspace depends on the sizes alone; a training loop asks for the same

@@ -106,6 +106,14 @@ class GradBucketer:
         rows = self.alloc_arena(count, torch.float32)
         return [rows[i, :self.total] for i in range(count)]
 
+    def alloc_mx4(self, P):
+        """Room for every rank's gradients in bucket order in 4 bits: a list
+        of P ``Mx4`` of ``total`` elements (bucket b of one is
+        ``x.narrow(b * bucket_elems, bucket_len(b))`` when buckets are a
+        multiple of 32 elements)."""
+        from .mx4 import Mx4
+        return [Mx4.empty(self.total, self.device) for _ in range(P)]
+
     def bucket_view(self, arena_row, b):
         """Bucket b of one rank's arena row (its live elements only)."""
         lo = b * self.bucket_elems

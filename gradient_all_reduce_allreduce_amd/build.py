@@ -28,7 +28,8 @@ PATTERNS = os.path.join(PKG, "hbm_patterns")     # HBM access-pattern benchmark
 SOURCES = ["api.cpp", "ring_reduce.hip", "ring_reduce_f32_f32.hip",
            "ring_reduce_f32_bf16.hip", "ring_reduce_bf16_f32.hip",
            "ring_reduce_bf16_bf16.hip", "ring_norm.hip", "ring_allgather.hip", "ring_step.hip",
-           "multi_tensor.hip", "bucket_copy.hip", "grad_norm.hip", "adamw.hip"]
+           "multi_tensor.hip", "bucket_copy.hip", "grad_norm.hip", "adamw.hip",
+           "mx4.hip", "mx4_reduce.hip", "adamw8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

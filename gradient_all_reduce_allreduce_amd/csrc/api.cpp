@@ -25,6 +25,7 @@
 #include "launch_copy.h"
 #include "launch_grads.h"
 #include "launch_multi.h"
+#include "launch_mx.h"
 #include "launch_step.h"
 
 namespace {
@@ -1526,14 +1527,24 @@ int ring_norm(ddp_reduce_op op, int32_t P, int32_t chunking, const void* const* 
     return ok();
 }
 
+// The moments of an AdamW step: float32 (`scales` null), or codes of 8 bits
+// with their blocks' scales.
+struct Moments {
+    void* const* m;
+    void* const* v;
+    uint8_t* const* scales;
+    int64_t seed;
+};
+
 int adamw_step(int32_t n_tensors, const int64_t* numels, const void* const* grads, ddp_dtype grad_dtype,
-               float* const* w, float* const* m, float* const* v, void* const* params, ddp_dtype param_dtype,
+               float* const* w, const Moments& moments, void* const* params, ddp_dtype param_dtype,
                double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
                const int64_t* step_dev, const float* norm, double max_norm, void* stream) {
+    const bool bits8 = moments.scales != nullptr;
     int s = check_list(n_tensors, numels);
     if (s) return s;
     if (!valid_dtype(grad_dtype) || !valid_dtype(param_dtype)) return fail(DDP_E_ARG, "unknown dtype");
-    if (grads == nullptr || w == nullptr || m == nullptr || v == nullptr)
+    if (grads == nullptr || w == nullptr || moments.m == nullptr || moments.v == nullptr)
         return fail(DDP_E_ARG, "NULL pointer argument");
     if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return fail(DDP_E_ARG, "lr and weight_decay must be finite");
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
@@ -1546,19 +1557,25 @@ int adamw_step(int32_t n_tensors, const int64_t* numels, const void* const* grad
     const int ges = elem_bytes(grad_dtype);
     const int pes = elem_bytes(param_dtype);
     std::vector<Span> spans;
-    spans.reserve(5 * static_cast<size_t>(n_tensors) + 2);
+    spans.reserve((bits8 ? 6 : 5) * static_cast<size_t>(n_tensors) + 2);
     // One stream after another: lists that lie in order in memory, each
     // behind the one before, then need no sorting.
     for (int32_t t = 0; t < n_tensors; ++t) {
         if ((s = check_tensor(grads[t], numels[t], ges, "grads", t))) return s;
         if (numels[t] > 0) spans.push_back(span_of(grads[t], numels[t] * ges, false, "grads", t));
     }
-    const struct { float* const* list; const char* what; } state[3] = {{w, "w"}, {m, "m"}, {v, "v"}};
+    const int mes = bits8 ? 1 : 4;
+    const struct { const void* const* list; int es; const char* what; } state[3] = {
+        {reinterpret_cast<const void* const*>(w), 4, "w"}, {moments.m, mes, "m"}, {moments.v, mes, "v"}};
     for (const auto& x : state) {
         for (int32_t t = 0; t < n_tensors; ++t) {
-            if ((s = check_tensor(x.list[t], numels[t], 4, x.what, t))) return s;
-            if (numels[t] > 0) spans.push_back(span_of(x.list[t], numels[t] * 4, true, x.what, t));
+            if ((s = check_tensor(x.list[t], numels[t], x.es, x.what, t))) return s;
+            if (numels[t] > 0) spans.push_back(span_of(x.list[t], numels[t] * x.es, true, x.what, t));
         }
+    }
+    for (int32_t t = 0; bits8 && t < n_tensors; ++t) {
+        if ((s = check_tensor(moments.scales[t], numels[t], 2, "scales", t))) return s;
+        if (numels[t] > 0) spans.push_back(span_of(moments.scales[t], 2 * ddp::mx_blocks(numels[t]), true, "scales", t));
     }
     for (int32_t t = 0; params != nullptr && t < n_tensors; ++t) {
         if ((s = check_tensor(params[t], numels[t], pes, "params", t))) return s;
@@ -1573,8 +1590,6 @@ int adamw_step(int32_t n_tensors, const int64_t* numels, const void* const* grad
     l.numels = numels;
     l.grads = grads;
     l.w = w;
-    l.m = m;
-    l.v = v;
     l.params = params;
     l.grad_bf16 = grad_dtype == DDP_BF16;
     l.param_bf16 = param_dtype == DDP_BF16;
@@ -1589,7 +1604,15 @@ int adamw_step(int32_t n_tensors, const int64_t* numels, const void* const* grad
     l.max_norm = static_cast<float>(norm != nullptr ? max_norm : 0.0);
     l.stream = stream;
     const char* msg = nullptr;
-    const int e = ddp::launch_adamw(l, &msg);
+    int e = 0;
+    if (bits8) {
+        e = ddp::launch_adamw8({l, reinterpret_cast<uint8_t* const*>(moments.m),
+                                reinterpret_cast<uint8_t* const*>(moments.v), moments.scales, moments.seed}, &msg);
+    } else {
+        l.m = reinterpret_cast<float* const*>(moments.m);
+        l.v = reinterpret_cast<float* const*>(moments.v);
+        e = ddp::launch_adamw(l, &msg);
+    }
     if (e != 0) return hip_fail(e, msg);
     return ok();
 }
@@ -1673,9 +1696,260 @@ int adamw_step_multi(int32_t n_tensors, const int64_t* numels, const void* const
                      double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
                      const int64_t* step_dev, const float* norm, double max_norm, void* stream) {
     return guarded([&] {
-        return adamw_step(n_tensors, numels, grads, grad_dtype, w, m, v, params, param_dtype, lr, beta1, beta2, eps,
+        const Moments moments = {reinterpret_cast<void* const*>(m), reinterpret_cast<void* const*>(v), nullptr, 0};
+        return adamw_step(n_tensors, numels, grads, grad_dtype, w, moments, params, param_dtype, lr, beta1, beta2, eps,
                           weight_decay, step, step_dev, norm, max_norm, stream);
     });
+}
+
+}  // extern "C"
+
+// ---- 4-bit gradients, 8-bit moments --------------------------------------------
+
+namespace {
+
+int64_t code_bytes(int64_t n) { return ddp::mx_blocks(n) * (DDP_MX_BLOCK / 2); }
+
+// P rows of values, each aligned to its elements.
+int check_rows(const void* const* rows, int32_t P, int es, const char* what) {
+    if (rows == nullptr) return fail(DDP_E_ARG, "%s is NULL", what);
+    for (int r = 0; r < P; ++r) {
+        if (rows[r] == nullptr) return fail(DDP_E_ARG, "%s[%d] is NULL", what, r);
+        if (reinterpret_cast<uintptr_t>(rows[r]) % es)
+            return fail(DDP_E_ALIGN, "%s[%d] is not aligned to its element size", what, r);
+    }
+    return DDP_OK;
+}
+
+// P coded rows: codes on 16 bytes, scales anywhere.
+int check_coded(const uint8_t* const* codes, const uint8_t* const* scales, int32_t P, const char* what) {
+    char name[40];
+    snprintf(name, sizeof name, "%s_codes", what);
+    if (const int s = check_ptr_array(reinterpret_cast<const void* const*>(codes), P, name)) return s;
+    snprintf(name, sizeof name, "%s_scales", what);
+    return check_rows(reinterpret_cast<const void* const*>(scales), P, 1, name);
+}
+
+// Between values and codes: `quantize` writes the codes, else the values.
+int mx4_rows(bool quantize, int32_t P, const void* const* values, int dtype, int64_t n, void* const* left,
+             int left_dtype, const uint8_t* const* codes, const uint8_t* const* scales, void* stream) {
+    int s = check_ranks(P);
+    if (s) return s;
+    if ((s = check_length(n, "n"))) return s;
+    if (!valid_dtype(dtype) || (left != nullptr && !valid_dtype(left_dtype))) return fail(DDP_E_ARG, "unknown dtype");
+    if (n == 0) return ok();
+    const char* const what = quantize ? "rank_in" : "rank_out";
+    if ((s = check_rows(values, P, elem_bytes(dtype), what))) return s;
+    if (left != nullptr && (s = check_rows(left, P, elem_bytes(left_dtype), "rank_residual"))) return s;
+    if ((s = check_coded(codes, scales, P, "rank"))) return s;
+    std::vector<Span> spans;
+    spans.reserve(4 * static_cast<size_t>(P));
+    ddp::Mx4Launch l{};
+    for (int r = 0; r < P; ++r) {
+        spans.push_back(span_of(values[r], n * elem_bytes(dtype), !quantize, what, r));
+        if (left != nullptr) spans.push_back(span_of(left[r], n * elem_bytes(left_dtype), true, "rank_residual", r));
+        spans.push_back(span_of(codes[r], code_bytes(n), quantize, "rank_codes", r));
+        spans.push_back(span_of(scales[r], ddp::mx_blocks(n), quantize, "rank_scales", r));
+        l.values[r] = values[r];
+        l.left[r] = left != nullptr ? left[r] : nullptr;
+        l.codes[r] = const_cast<uint8_t*>(codes[r]);
+        l.scales[r] = const_cast<uint8_t*>(scales[r]);
+    }
+    if ((s = check_written(spans))) return s;
+    l.P = P;
+    l.n = n;
+    l.bf16 = dtype == DDP_BF16;
+    l.left_type = left == nullptr ? 0 : (left_dtype == DDP_BF16 ? 2 : 1);
+    l.stream = stream;
+    const char* msg = nullptr;
+    const int e = quantize ? ddp::launch_mx4_quantize(l, &msg) : ddp::launch_mx4_dequantize(l, &msg);
+    if (e != 0) return hip_fail(e, msg);
+    return ok();
+}
+
+// The all-reduce of coded rows, into values (`out_scales` null) or codes.
+int mx4_reduce(ddp_reduce_op op, int32_t P, const uint8_t* const* codes, const uint8_t* const* scales, int64_t n,
+               int32_t n_out, void* const* out, bool coded, int out_dtype, uint8_t* const* out_scales, void* left,
+               int left_dtype, float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (op != DDP_SUM && op != DDP_MEAN) return fail(DDP_E_ARG, "unknown reduce op %d", op);
+    int s = check_ranks(P);
+    if (s) return s;
+    if ((s = check_length(n, "n"))) return s;
+    if (n_out != 1 && n_out != P) return fail(DDP_E_ARG, "n_out = %d, must be 1 or P", n_out);
+    if (!coded && !valid_dtype(out_dtype)) return fail(DDP_E_ARG, "unknown output dtype %d", out_dtype);
+    if (left != nullptr && !valid_dtype(left_dtype)) return fail(DDP_E_ARG, "unknown residual dtype %d", left_dtype);
+    if (norm != nullptr && (s = check_norm_ptr(norm))) return s;
+    const char* msg = nullptr;
+    if (n == 0) {   // no element, no buffer to look at: the norm is 0
+        const int e = norm != nullptr ? ddp::launch_norm_of(nullptr, 0, nullptr, norm, stream, &msg) : 0;
+        return e != 0 ? hip_fail(e, msg) : ok();
+    }
+    if ((s = check_coded(codes, scales, P, "rank"))) return s;
+    const int oes = coded ? 1 : elem_bytes(out_dtype);
+    if (coded) {
+        if ((s = check_coded(reinterpret_cast<const uint8_t* const*>(out), out_scales, n_out, "out"))) return s;
+    } else if ((s = check_rows(out, n_out, oes, "rank_out"))) {
+        return s;
+    }
+    const int64_t groups = ddp::mx4_reduce_workgroups(n);
+    const int64_t need = norm != nullptr ? norm_workspace(groups) : 0;
+    if (norm != nullptr && (s = check_workspace(workspace, workspace_bytes, need))) return s;
+    // Coded rows may be written over the ones they came from: a block is read
+    // from every rank before any is written.  Element sizes of 1 and 2 keep codes
+    // from passing for scales.
+    std::vector<Buf> bufs;
+    const auto add = [&bufs](const void* p, int64_t bytes, int es, const char* what, int index) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        bufs.push_back({lo, lo + static_cast<uintptr_t>(bytes), es, what, index});
+    };
+    const int64_t blocks = ddp::mx_blocks(n);
+    for (int r = 0; r < P; ++r) {
+        add(codes[r], code_bytes(n), 1, "rank_codes", r);
+        add(scales[r], blocks, 2, "rank_scales", r);
+    }
+    for (int r = 0; r < n_out; ++r) {
+        if (coded) {
+            add(out[r], code_bytes(n), 1, "out_codes", r);
+            add(out_scales[r], blocks, 2, "out_scales", r);
+        } else {
+            add(out[r], n * oes, 16 * oes, "rank_out", r);
+        }
+    }
+    if ((s = check_overlaps(bufs))) return s;
+    const Span alone[3] = {span_of(left, left != nullptr ? n * elem_bytes(left_dtype) : 0, true, "residual", 0),
+                           span_of(norm, norm != nullptr ? sizeof(float) : 0, true, "norm", 0),
+                           span_of(workspace, need, true, "workspace", 0)};
+    if (left != nullptr && reinterpret_cast<uintptr_t>(left) % elem_bytes(left_dtype))
+        return fail(DDP_E_ALIGN, "residual is not aligned to its element size");
+    for (int i = 0; i < 3; ++i) {
+        const Span& x = alone[i];
+        if (x.lo == x.hi) continue;
+        for (const Buf& b : bufs)
+            if (x.lo < b.hi && b.lo < x.hi) return fail(DDP_E_OVERLAP, "%s overlaps %s[%d]", x.what, b.what, b.index);
+        for (int j = 0; j < i; ++j)
+            if (x.lo < alone[j].hi && alone[j].lo < x.hi)
+                return fail(DDP_E_OVERLAP, "%s overlaps %s", x.what, alone[j].what);
+    }
+
+    ddp::Mx4Reduce l{};
+    l.P = P;
+    l.mean = op == DDP_MEAN;
+    l.n = n;
+    for (int r = 0; r < P; ++r) {
+        l.codes[r] = codes[r];
+        l.scales[r] = scales[r];
+    }
+    l.n_out = n_out;
+    l.out_type = coded ? 2 : (out_dtype == DDP_BF16 ? 1 : 0);
+    for (int r = 0; r < n_out; ++r) {
+        l.out[r] = out[r];
+        l.out_scales[r] = coded ? out_scales[r] : nullptr;
+    }
+    l.left = left;
+    l.left_type = left == nullptr ? 0 : (left_dtype == DDP_BF16 ? 2 : 1);
+    if (norm != nullptr) {
+        l.partials = static_cast<double*>(workspace);
+        if (groups > ddp::kNormFoldOver) l.zero = reinterpret_cast<uint64_t*>(l.partials + groups + ddp::kNormFold);
+    }
+    l.stream = stream;
+    int e = ddp::launch_mx4_reduce(l, &msg);
+    if (e == 0 && norm != nullptr) e = ddp::launch_norm_of(l.partials, groups, l.partials + groups, norm, stream, &msg);
+    if (e != 0) return hip_fail(e, msg);
+    return ok();
+}
+
+int adamw8_read(int32_t n_tensors, const int64_t* numels, const uint8_t* const* m, const uint8_t* const* v,
+                const uint8_t* const* scales, void* const* m_out, void* const* v_out, int out_dtype, void* stream) {
+    int s = check_list(n_tensors, numels);
+    if (s) return s;
+    if (!valid_dtype(out_dtype)) return fail(DDP_E_ARG, "unknown dtype");
+    if (m == nullptr || v == nullptr || scales == nullptr || m_out == nullptr || v_out == nullptr)
+        return fail(DDP_E_ARG, "NULL pointer argument");
+    const int es = elem_bytes(out_dtype);
+    std::vector<Span> spans;
+    spans.reserve(5 * static_cast<size_t>(n_tensors));
+    const struct { const void* const* list; int es; bool written; const char* what; } lists[5] = {
+        {reinterpret_cast<const void* const*>(m), 1, false, "m"},
+        {reinterpret_cast<const void* const*>(v), 1, false, "v"},
+        {reinterpret_cast<const void* const*>(scales), 2, false, "scales"},
+        {m_out, es, true, "m_out"},
+        {v_out, es, true, "v_out"}};
+    for (const auto& x : lists) {
+        for (int32_t t = 0; t < n_tensors; ++t) {
+            if ((s = check_tensor(x.list[t], numels[t], x.es, x.what, t))) return s;
+            const int64_t count = x.es == 2 && !x.written ? ddp::mx_blocks(numels[t]) : numels[t];
+            if (numels[t] > 0) spans.push_back(span_of(x.list[t], count * x.es, x.written, x.what, t));
+        }
+    }
+    if ((s = check_written(spans))) return s;
+    const char* msg = nullptr;
+    const int e = ddp::launch_adamw8_read({n_tensors, numels, m, v, scales, m_out, v_out, out_dtype == DDP_BF16, stream},
+                                          &msg);
+    if (e != 0) return hip_fail(e, msg);
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx4_quantize(int32_t P, const void* const* rank_in, ddp_dtype in_dtype, int64_t n, void* const* rank_residual,
+                 ddp_dtype residual_dtype, uint8_t* const* rank_codes, uint8_t* const* rank_scales, void* stream) {
+    return guarded([&] {
+        return mx4_rows(true, P, rank_in, in_dtype, n, rank_residual, residual_dtype, rank_codes, rank_scales, stream);
+    });
+}
+
+int mx4_dequantize(int32_t P, const uint8_t* const* rank_codes, const uint8_t* const* rank_scales, int64_t n,
+                   void* const* rank_out, ddp_dtype out_dtype, void* stream) {
+    return guarded([&] {
+        return mx4_rows(false, P, rank_out, out_dtype, n, nullptr, DDP_F32, rank_codes, rank_scales, stream);
+    });
+}
+
+int allreduce_mx4(ddp_reduce_op op, int32_t P, const uint8_t* const* rank_codes, const uint8_t* const* rank_scales,
+                  int64_t n, int32_t n_out, void* const* rank_out, ddp_dtype out_dtype, float* norm, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+    return guarded([&] {
+        return mx4_reduce(op, P, rank_codes, rank_scales, n, n_out, rank_out, false, out_dtype, nullptr, nullptr, DDP_F32,
+                          norm, workspace, workspace_bytes, stream);
+    });
+}
+
+int allreduce_mx4_coded(ddp_reduce_op op, int32_t P, const uint8_t* const* rank_codes,
+                        const uint8_t* const* rank_scales, int64_t n, int32_t n_out, uint8_t* const* out_codes,
+                        uint8_t* const* out_scales, void* residual, ddp_dtype residual_dtype, float* norm,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+    return guarded([&] {
+        return mx4_reduce(op, P, rank_codes, rank_scales, n, n_out, reinterpret_cast<void* const*>(out_codes), true,
+                          DDP_F32, out_scales, residual, residual_dtype, norm, workspace, workspace_bytes, stream);
+    });
+}
+
+int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes) {
+    if (const int s = check_length(n, "n")) return s;
+    if (bytes == nullptr) return fail(DDP_E_ARG, "bytes is NULL");
+    *bytes = norm_workspace(ddp::mx4_reduce_workgroups(n));
+    return ok();
+}
+
+int adamw8_step_multi(int32_t n_tensors, const int64_t* numels, const void* const* grads, ddp_dtype grad_dtype,
+                      float* const* w, uint8_t* const* m, uint8_t* const* v, uint8_t* const* scales,
+                      void* const* params, ddp_dtype param_dtype, double lr, double beta1, double beta2, double eps,
+                      double weight_decay, int64_t step, const int64_t* step_dev, int64_t seed, const float* norm,
+                      double max_norm, void* stream) {
+    if (scales == nullptr) return fail(DDP_E_ARG, "NULL pointer argument");
+    return guarded([&] {
+        const Moments moments = {reinterpret_cast<void* const*>(m), reinterpret_cast<void* const*>(v), scales, seed};
+        return adamw_step(n_tensors, numels, grads, grad_dtype, w, moments, params, param_dtype, lr, beta1, beta2, eps,
+                          weight_decay, step, step_dev, norm, max_norm, stream);
+    });
+}
+
+int adamw8_read_multi(int32_t n_tensors, const int64_t* numels, const uint8_t* const* m, const uint8_t* const* v,
+                      const uint8_t* const* scales, void* const* m_out, void* const* v_out, ddp_dtype out_dtype,
+                      void* stream) {
+    return guarded([&] { return adamw8_read(n_tensors, numels, m, v, scales, m_out, v_out, out_dtype, stream); });
 }
 
 }  // extern "C"

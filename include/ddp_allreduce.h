@@ -973,6 +973,162 @@ int adamw_step_multi(int32_t n_tensors, const int64_t* numels, const void* const
                      const int64_t* step_dev, const float* norm, double max_norm,
                      void* stream);
 
+/* Elements per block of the microscaled formats below. */
+#define DDP_MX_BLOCK 32
+
+/*
+ * mx4_quantize / mx4_dequantize -- gradients in microscaled 4-bit floating
+ * point, and back.
+ *
+ * Less data for the all-reduce to move: the pages count its traffic in model
+ * sizes per step ("Distributed Training", "Communication costs"), and a
+ * gradient coded so is 17/128 of its float32 size.  A block is 32 consecutive
+ * elements of a row (a row's last one may be shorter).  It has one scale byte
+ * s, which stands for 2^(s - 127), and 16 bytes of codes, element 2k of the
+ * row in the low half of byte k: sign, 2 bits of exponent, 1 of mantissa, for
+ * 0, 0.5, 1, 1.5, 2, 3, 4 and 6 (the formats E2M1 and E8M0 of the OCP
+ * microscaling specification).
+ *
+ * mx4_quantize, for the elements of a block, in float32:
+ *     t = gradient + residual          one rounding (t = gradient without one)
+ *     2^(s - 127) = the smallest power of two, from 2^-126, with max |t| < 7 * it
+ *     code = the level nearest to t / 2^(s - 127), ties to the even code
+ *     residual = t - the code's value  exact (then rounded for bf16 residuals)
+ * Every code is off by half a step at most.  What a step rounds away goes into
+ * the next one's gradient, so that over many steps what is sent is what was
+ * computed; residuals begin at zero.
+ * A block with an infinity, a NaN or a |t| of 1.75 * 2^127 or more gets s = 255
+ * and zero codes, all its elements decode to NaN, and its residual stays as
+ * it was.  Codes behind the row's end are zero.
+ *
+ * mx4_dequantize writes the codes' values: exact in float32 but for those over
+ * its range (infinite) and exact in bf16 for scales that mx4_quantize gives
+ * (otherwise rounded to nearest even).
+ *
+ *   P             rows, 1 .. 16: the ranks' gradients of one bucket or arena
+ *   rank_in       host array [P], elements of in_dtype
+ *   n             elements of each row, 0 .. 2^40
+ *   rank_residual host array [P], read and written, residual_dtype; or NULL
+ *   rank_codes    host array [P], 16-byte aligned, 16 bytes for each block
+ *   rank_scales   host array [P], a byte for each block, at any address
+ *   rank_out      host array [P] receiving elements of out_dtype
+ * Values need only the alignment of their element type.  A part of a row that
+ * begins at a multiple of 32 elements may be coded on its own (a bucket, as
+ * soon as it is full) with the same result.  Nothing written may overlap any
+ * other buffer of the call.  Nothing is looked at when n = 0.
+ * Errors: DDP_E_ARG, DDP_E_ALIGN, DDP_E_OVERLAP, DDP_E_HIP.
+ */
+int mx4_quantize(int32_t P, const void* const* rank_in, ddp_dtype in_dtype, int64_t n,
+                 void* const* rank_residual, ddp_dtype residual_dtype,
+                 uint8_t* const* rank_codes, uint8_t* const* rank_scales, void* stream);
+
+int mx4_dequantize(int32_t P, const uint8_t* const* rank_codes,
+                   const uint8_t* const* rank_scales, int64_t n, void* const* rank_out,
+                   ddp_dtype out_dtype, void* stream);
+
+/*
+ * allreduce_mx4 / allreduce_mx4_coded -- the all-reduce of P rank gradients in
+ * the 4-bit format above.
+ *
+ *     g = q_0 + q_1 + ... + q_{P-1};   g = g / P with Mean
+ *
+ * the ranks' decoded values in float32, one rounding per addition, in rank
+ * order: a block's codes travel whole, to an owner that has all P copies and
+ * adds them, so unlike the ring's the order does not depend on the chunk.
+ * allreduce_mx4 writes g as float32 or bf16 (nearest even) values;
+ * allreduce_mx4_coded codes it again by the rules of mx4_quantize, with one
+ * residual, the owner's, or none.  A NaN block of one rank is NaN in the
+ * result.
+ *
+ *   n_out        P: every rank receives the result; 1: one copy
+ *   rank_out     host array [n_out], elements of out_dtype, aligned to them
+ *   out_codes, out_scales  host arrays [n_out]; a codes (scales) buffer may be
+ *                one of the inputs' exactly (in place)
+ *   residual     n elements of residual_dtype, read and written, or NULL
+ *   norm         device pointer to one float, receives the 2-norm of the
+ *                result as it is written (squares and sums float64, rounded
+ *                once); or NULL
+ *   workspace    with norm: device memory, 16-byte aligned, of at least the
+ *                bytes allreduce_mx4_workspace_bytes gives; calls that may run
+ *                at the same time need one each
+ *   other arguments as for mx4_quantize; with n = 0 the norm is 0 and nothing
+ *   else is looked at
+ * Errors: DDP_E_ARG, DDP_E_ALIGN, DDP_E_OVERLAP, DDP_E_HIP.
+ */
+int allreduce_mx4(ddp_reduce_op op, int32_t P, const uint8_t* const* rank_codes,
+                  const uint8_t* const* rank_scales, int64_t n, int32_t n_out,
+                  void* const* rank_out, ddp_dtype out_dtype, float* norm, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
+int allreduce_mx4_coded(ddp_reduce_op op, int32_t P, const uint8_t* const* rank_codes,
+                        const uint8_t* const* rank_scales, int64_t n, int32_t n_out,
+                        uint8_t* const* out_codes, uint8_t* const* out_scales, void* residual,
+                        ddp_dtype residual_dtype, float* norm, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/*
+ * allreduce_mx4_workspace_bytes -- host only: the workspace of the two calls
+ * above when they leave a norm, in *bytes (8 for each 512 elements, and some).
+ * Errors: DDP_E_ARG.
+ */
+int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes);
+
+/*
+ * adamw8_step_multi -- adamw_step_multi with the moments in 8 bits: 2.06
+ * bytes an element for both instead of 8.
+ *
+ * The step is adamw_step_multi's, on decoded moments, and the weights take the
+ * new moments before these are rounded.  A block is 32 consecutive elements of
+ * a tensor, with two scale bytes, s_m then s_v:
+ *   m   one byte: sign, 4 bits of exponent, 3 of mantissa (the format E4M3 of
+ *       the OCP microscaling specification, up to 448), times 2^(s_m - 127), s_m
+ *       the smallest, from 1, that holds the block's maximum
+ *   v   one byte c: (1 + (c & 7) / 8) * 2^((c >> 3) - 31) * 2^(s_v - 127), at most
+ *       1.875 scales, s_v the smallest, from 32, that holds the block's
+ *       maximum; s_v = 0 and zero codes for a block of zeros.  No code is
+ *       zero: in a block with a larger element even 0 becomes 2^-31 scales, so
+ *       that no first moment outlives its second one.
+ * Fresh moments are zero bytes, codes and scales.
+ * A moment changes by less than a step of its code, and rounded to nearest
+ * would stop there, so it is rounded at random, up with the probability of the
+ * part that is cut off (to 1/65536 of a step): a rounded moment is right on
+ * average.  The 16 random bits of each moment are a hash of seed, step, the
+ * tensor's number in the call and the element's in its tensor: the same call
+ * gives the same bits, on any stream and in any replay.  Ranks that keep
+ * identical replicas need the same seed.
+ * A block of m that meets an infinity or NaN becomes NaN as a whole, one of v
+ * that passes float32 infinite.
+ *
+ *   m, v         HOST arrays [n_tensors] of pointers to one byte per element, at
+ *                any address, updated in place
+ *   scales       HOST array [n_tensors] of pointers to two bytes per block,
+ *                2-byte aligned, updated in place
+ *   seed         any value
+ *   other arguments as for adamw_step_multi
+ * Errors: as for adamw_step_multi.
+ */
+int adamw8_step_multi(int32_t n_tensors, const int64_t* numels, const void* const* grads,
+                      ddp_dtype grad_dtype, float* const* w, uint8_t* const* m,
+                      uint8_t* const* v, uint8_t* const* scales, void* const* params,
+                      ddp_dtype param_dtype, double lr, double beta1, double beta2, double eps,
+                      double weight_decay, int64_t step, const int64_t* step_dev, int64_t seed,
+                      const float* norm, double max_norm, void* stream);
+
+/*
+ * adamw8_read_multi -- the values of 8-bit moments, e.g. for a checkpoint in
+ * 32 bits or to go on with adamw_step_multi.
+ *
+ *   m_out, v_out HOST arrays [n_tensors] receiving elements of out_dtype (both
+ *                types hold the values exactly, but for bf16 below 2^-126)
+ *   other arguments as for adamw8_step_multi (read only)
+ * Nothing written may overlap any other buffer of the call.
+ * Errors: DDP_E_ARG, DDP_E_ALIGN, DDP_E_OVERLAP, DDP_E_HIP.
+ */
+int adamw8_read_multi(int32_t n_tensors, const int64_t* numels, const uint8_t* const* m,
+                      const uint8_t* const* v, const uint8_t* const* scales,
+                      void* const* m_out, void* const* v_out, ddp_dtype out_dtype,
+                      void* stream);
+
 /* Kernel families whose launch shape ddp_set_wg_per_cu can override. */
 typedef enum ddp_kernel_family {
     DDP_KF_RING = 0,            /* allreduce_ring_emulated, allreduce_ring_norm */

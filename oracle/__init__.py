@@ -35,6 +35,8 @@ Modules:
     zero    -- ZeRO stage 1: reduce-scatter, the owner's optimizer step,
                all-gather of the updated parameters
     grads   -- the global gradient norm, clipping by it, the AdamW step
+    mx      -- microscaled 4-bit gradients and their all-reduce, the AdamW step
+               with 8-bit moments
 
 Parity status of each function is stated in its module header.
 """
@@ -49,6 +51,7 @@ from .bf16 import bf16_bits_to_f32, f32_to_bf16_bits
 from .sgd import sgd_momentum
 from .bucket import bucket_plan, pack, unpack
 from .grads import adamw, adamw64, clip_factor, clip_factor64, grad_norm
+from . import mx
 
 __all__ = [
     "SUM", "MEAN", "chunk_length", "chunk_owners", "chunk_start_ranks",
@@ -56,5 +59,5 @@ __all__ = [
     "ring_allreduce_sampled", "bf16_bits_to_f32", "f32_to_bf16_bits",
     "sgd_momentum", "bucket_plan", "pack", "unpack", "tree_allreduce", "tree_parents",
     "hierarchical_allreduce", "zero1_sgd_step", "adamw", "adamw64", "clip_factor",
-    "clip_factor64", "grad_norm",
+    "clip_factor64", "grad_norm", "mx",
 ]

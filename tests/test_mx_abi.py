@@ -1,0 +1,315 @@
+"""Refusals of the 4-bit gradient and 8-bit moment calls: host only, every
+call returns before any launch."""
+
+import ctypes
+
+import pytest
+import torch
+
+ddp = pytest.importorskip("gradient_all_reduce_allreduce_amd")
+from gradient_all_reduce_allreduce_amd import _native as N  # noqa: E402
+from gradient_all_reduce_allreduce_amd.api import DdpError  # noqa: E402
+
+BASE = 0x7f0000000000          # never dereferenced
+STEP = 1 << 20
+WS, NORM, STEPS = BASE + (1 << 36), BASE + (1 << 37), BASE + (1 << 38)
+NAN, INF = float("nan"), float("inf")
+
+
+def at(k, off=0):
+    return BASE + k * STEP + off
+
+
+def refused(fn, args, status, text=None):
+    with pytest.raises(DdpError) as e:
+        fn(**args)
+    assert e.value.status == status, e.value
+    if text:
+        assert text in str(e.value)
+
+
+def quantize_args(**change):
+    a = dict(P=2, rank_in=[at(0), at(1)], in_dtype=ddp.F32, n=1000, rank_residual=[at(2), at(3)], residual_dtype=ddp.BF16,
+             rank_codes=[at(4), at(5)], rank_scales=[at(6), at(7)])
+    a.update(change)
+    return a
+
+
+def dequantize_args(**change):
+    a = dict(P=2, rank_codes=[at(4), at(5)], rank_scales=[at(6), at(7)], n=1000, rank_out=[at(0), at(1)], out_dtype=ddp.F32)
+    a.update(change)
+    return a
+
+
+def reduce_args(**change):
+    a = dict(op="mean", P=2, rank_codes=[at(4), at(5)], rank_scales=[at(6), at(7)], n=1000, rank_out=[at(0), at(1)],
+             out_dtype=ddp.F32, norm=NORM, workspace=WS, workspace_bytes=16)
+    a.update(change)
+    return a
+
+
+def coded_args(**change):
+    a = dict(op="mean", P=2, rank_codes=[at(4), at(5)], rank_scales=[at(6), at(7)], n=1000, out_codes=[at(8), at(9)],
+             out_scales=[at(10), at(11)], residual=at(2), residual_dtype=ddp.F32, norm=NORM, workspace=WS,
+             workspace_bytes=16)
+    a.update(change)
+    return a
+
+
+def adamw_args(**change):
+    a = dict(numels=[100, 0, 7], grads=[at(0), 0, at(2)], grad_dtype=ddp.BF16, w=[at(3), 0, at(4)],
+             m=[at(5, 1), 0, at(6)], v=[at(7), 0, at(8, 3)], scales=[at(11, 2), 0, at(12)], params=[at(9), 0, at(10)],
+             param_dtype=ddp.BF16, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, step_dev=None,
+             seed=0, norm=NORM, max_norm=1.0)
+    a.update(change)
+    return a
+
+
+def read_args(**change):
+    a = dict(numels=[100, 0, 7], m=[at(5, 1), 0, at(6)], v=[at(7), 0, at(8, 3)], scales=[at(11, 2), 0, at(12)],
+             m_out=[at(0), 0, at(1)], v_out=[at(2), 0, at(3)], out_dtype=ddp.F32)
+    a.update(change)
+    return a
+
+
+ROWS = [
+    (dict(P=0), N.DDP_E_ARG, "P = 0"),
+    (dict(P=17), N.DDP_E_ARG, "P = 17"),
+    (dict(n=-1), N.DDP_E_ARG, "negative"),
+    (dict(n=(1 << 40) + 1), N.DDP_E_ARG, "2^40"),
+    (dict(rank_codes=None), N.DDP_E_ARG, "rank_codes"),
+    (dict(rank_codes=[at(4), 0]), N.DDP_E_ARG, "rank_codes[1]"),
+    (dict(rank_codes=[at(4, 8), at(5)]), N.DDP_E_ALIGN, "rank_codes[0]"),
+    (dict(rank_scales=None), N.DDP_E_ARG, "rank_scales"),
+    (dict(rank_scales=[0, at(7)]), N.DDP_E_ARG, "rank_scales[0]"),
+]
+
+
+@pytest.mark.parametrize("change,status,text", ROWS + [
+    (dict(in_dtype=3), N.DDP_E_ARG, "dtype"),
+    (dict(residual_dtype=-1), N.DDP_E_ARG, "dtype"),
+    (dict(rank_in=None), N.DDP_E_ARG, "rank_in"),
+    (dict(rank_in=[at(0), at(1, 2)]), N.DDP_E_ALIGN, "rank_in[1]"),
+    (dict(rank_residual=[at(2, 1), at(3)]), N.DDP_E_ALIGN, "rank_residual[0]"),
+    (dict(rank_residual=[at(2), 0]), N.DDP_E_ARG, "rank_residual[1]"),
+    (dict(rank_codes=[at(4), at(4)]), N.DDP_E_OVERLAP, None),               # both ranks' codes
+    (dict(rank_codes=[at(4), at(4, 496)]), N.DDP_E_OVERLAP, None),          # by one 16-byte line
+    (dict(rank_codes=[at(0, 3984), at(5)]), N.DDP_E_OVERLAP, None),         # over the gradient's end
+    (dict(rank_scales=[at(6), at(6, 31)]), N.DDP_E_OVERLAP, None),
+    (dict(rank_residual=[at(0), at(3)]), N.DDP_E_OVERLAP, None),            # the gradient as its residual
+    (dict(rank_residual=[at(2), at(2)]), N.DDP_E_OVERLAP, None),            # one residual for two ranks
+])
+def test_quantize_refusals(change, status, text):
+    refused(ddp.mx4_quantize_rows, quantize_args(**change), status, text)
+
+
+@pytest.mark.parametrize("change,status,text", ROWS + [
+    (dict(out_dtype=3), N.DDP_E_ARG, "dtype"),
+    (dict(rank_out=None), N.DDP_E_ARG, "rank_out"),
+    (dict(rank_out=[at(0, 2), at(1)]), N.DDP_E_ALIGN, "rank_out[0]"),
+    (dict(rank_out=[at(0), at(0)]), N.DDP_E_OVERLAP, None),
+    (dict(rank_out=[at(0), at(5, 508)]), N.DDP_E_OVERLAP, None),
+])
+def test_dequantize_refusals(change, status, text):
+    refused(ddp.mx4_dequantize_rows, dequantize_args(**change), status, text)
+
+
+NORMS = [
+    (dict(op=2), N.DDP_E_ARG, None),
+    (dict(norm=NORM + 2), N.DDP_E_ALIGN, "norm"),
+    (dict(workspace=None), N.DDP_E_ARG, "workspace"),
+    (dict(workspace_bytes=15), N.DDP_E_ARG, "workspace"),
+    (dict(workspace=WS + 8), N.DDP_E_ALIGN, "workspace"),
+    (dict(norm=WS + 12), N.DDP_E_OVERLAP, None),
+    (dict(norm=at(4, 16)), N.DDP_E_OVERLAP, None),
+    (dict(workspace=at(6, 16)), N.DDP_E_OVERLAP, None),
+]
+
+
+@pytest.mark.parametrize("change,status,text", ROWS + [x for x in NORMS if "op" not in x[0]] + [
+    (dict(out_dtype=9), N.DDP_E_ARG, "dtype"),
+    (dict(P=3, rank_codes=[at(4), at(5), at(12)], rank_scales=[at(6), at(7), at(13)]), N.DDP_E_ARG, "n_out"),
+    (dict(rank_out=[at(0), 0]), N.DDP_E_ARG, "rank_out[1]"),
+    (dict(rank_out=[at(0), at(1, 2)]), N.DDP_E_ALIGN, "rank_out[1]"),
+    (dict(rank_out=[at(0), at(0, 4)]), N.DDP_E_OVERLAP, None),
+    (dict(rank_out=[at(4), at(1)]), N.DDP_E_OVERLAP, None),                 # values over codes
+])
+def test_reduce_refusals(change, status, text):
+    refused(ddp.allreduce_mx4_rows, reduce_args(**change), status, text)
+
+
+def test_unknown_op():
+    with pytest.raises(KeyError):
+        ddp.allreduce_mx4_rows(**reduce_args(op="max"))
+    null = ctypes.cast(None, ctypes.POINTER(ctypes.c_void_p))
+    assert N.lib().allreduce_mx4(7, 2, null, null, 0, 1, null, 0, None, None, 0, None) == N.DDP_E_ARG
+
+
+@pytest.mark.parametrize("change,status,text", ROWS + [x for x in NORMS if "op" not in x[0]] + [
+    (dict(residual_dtype=9), N.DDP_E_ARG, "dtype"),
+    (dict(residual=at(2, 2)), N.DDP_E_ALIGN, "residual"),
+    (dict(residual=at(9)), N.DDP_E_OVERLAP, "residual"),
+    (dict(residual=WS), N.DDP_E_OVERLAP, None),
+    (dict(out_codes=[at(8), at(9, 4)]), N.DDP_E_ALIGN, "out_codes[1]"),
+    (dict(out_codes=[at(8), 0]), N.DDP_E_ARG, "out_codes[1]"),
+    (dict(out_scales=[at(10), 0]), N.DDP_E_ARG, "out_scales[1]"),
+    (dict(out_codes=[at(4, 16), at(9)]), N.DDP_E_OVERLAP, None),            # inside an input, not on it
+    (dict(out_scales=[at(6, 1), at(11)]), N.DDP_E_OVERLAP, None),
+    (dict(out_scales=[at(10), at(9)]), N.DDP_E_OVERLAP, None),              # scales over codes
+])
+def test_coded_reduce_refusals(change, status, text):
+    refused(ddp.allreduce_mx4_coded, coded_args(**change), status, text)
+
+
+def test_coded_reduce_lists():
+    with pytest.raises(ValueError):
+        ddp.allreduce_mx4_coded(**coded_args(out_scales=[at(10)]))
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (dict(numels=[100, -1, 7]), N.DDP_E_ARG, "negative"),
+    (dict(grads=[0, 0, at(2)]), N.DDP_E_ARG, "grads[0]"),
+    (dict(grads=[at(0, 1), 0, at(2)]), N.DDP_E_ALIGN, "grads[0]"),
+    (dict(w=[at(3, 2), 0, at(4)]), N.DDP_E_ALIGN, "w[0]"),
+    (dict(m=[at(5), 0, 0]), N.DDP_E_ARG, "m[2]"),
+    (dict(v=[0, 0, at(8)]), N.DDP_E_ARG, "v[0]"),
+    (dict(scales=[0, 0, at(12)]), N.DDP_E_ARG, "scales[0]"),
+    (dict(scales=[at(11, 1), 0, at(12)]), N.DDP_E_ALIGN, "scales[0]"),
+    (dict(m=[at(5), 0, at(5, 99)]), N.DDP_E_OVERLAP, None),
+    (dict(v=[at(5, 100), 0, at(8)]), N.DDP_E_OVERLAP, None),                # one byte into m
+    (dict(scales=[at(7, 98), 0, at(12)]), N.DDP_E_OVERLAP, None),
+    (dict(scales=[at(11), 0, at(11, 6)]), N.DDP_E_OVERLAP, None),           # four blocks are eight bytes
+    (dict(params=[at(3), 0, at(10)]), N.DDP_E_OVERLAP, None),
+    (dict(grad_dtype=4), N.DDP_E_ARG, "dtype"),
+    (dict(param_dtype=4), N.DDP_E_ARG, "dtype"),
+    (dict(lr=INF), N.DDP_E_ARG, "lr"),
+    (dict(beta1=1.0), N.DDP_E_ARG, "beta1"),
+    (dict(beta2=-0.1), N.DDP_E_ARG, "beta2"),
+    (dict(eps=NAN), N.DDP_E_ARG, "eps"),
+    (dict(step=0), N.DDP_E_ARG, "step"),
+    (dict(step_dev=STEPS + 4), N.DDP_E_ALIGN, "step_dev"),
+    (dict(step_dev=at(11, 4)), N.DDP_E_ALIGN, None),
+    (dict(step_dev=at(5, 8)), N.DDP_E_OVERLAP, None),
+    (dict(norm=NORM + 1), N.DDP_E_ALIGN, "norm"),
+    (dict(norm=at(12)), N.DDP_E_OVERLAP, None),
+    (dict(max_norm=-1.0), N.DDP_E_ARG, "max_norm"),
+])
+def test_adamw8_refusals(change, status, text):
+    refused(ddp.adamw8_step_multi, adamw_args(**change), status, text)
+
+
+def test_adamw8_null_lists():
+    assert N.lib().adamw8_step_multi(1, (ctypes.c_int64 * 1)(5), N.pointer_array([at(0)]), 0, N.pointer_array([at(1)]),
+                                     N.pointer_array([at(2)]), N.pointer_array([at(3)]), None, None, 0, 1e-3, 0.9, 0.9,
+                                     1e-8, 0.0, 1, None, 0, None, 0.0, None) == N.DDP_E_ARG
+    with pytest.raises(ValueError):
+        ddp.adamw8_step_multi(**adamw_args(scales=[at(11)]))
+    with pytest.raises(ValueError):
+        ddp.adamw8_read_multi(**read_args(v_out=[at(2)]))
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (dict(numels=[100, 1 << 41, 7]), N.DDP_E_ARG, "2^40"),
+    (dict(out_dtype=2), N.DDP_E_ARG, "dtype"),
+    (dict(m=[0, 0, at(6)]), N.DDP_E_ARG, "m[0]"),
+    (dict(scales=[at(11, 1), 0, at(12)]), N.DDP_E_ALIGN, "scales[0]"),
+    (dict(m_out=[at(0, 2), 0, at(1)]), N.DDP_E_ALIGN, "m_out[0]"),
+    (dict(v_out=[at(0, 396), 0, at(3)]), N.DDP_E_OVERLAP, None),
+    (dict(v_out=[at(7), 0, at(3)]), N.DDP_E_OVERLAP, None),
+    (dict(m_out=[at(11), 0, at(1)]), N.DDP_E_OVERLAP, None),
+])
+def test_read_refusals(change, status, text):
+    refused(ddp.adamw8_read_multi, read_args(**change), status, text)
+
+
+def test_workspace():
+    assert ddp.allreduce_mx4_workspace_bytes(0) == 0
+    assert ddp.allreduce_mx4_workspace_bytes(1) == 8
+    assert ddp.allreduce_mx4_workspace_bytes(513) == 16
+    with pytest.raises(DdpError):
+        ddp.allreduce_mx4_workspace_bytes(-1)
+    with pytest.raises(DdpError):
+        ddp.allreduce_mx4_workspace_bytes((1 << 40) + 1)
+    assert N.lib().allreduce_mx4_workspace_bytes(5, None) == N.DDP_E_ARG
+
+
+def test_nothing_to_do_without_buffers():
+    null = ctypes.cast(None, ctypes.POINTER(ctypes.c_void_p))
+    lib = N.lib()
+    assert lib.mx4_quantize(2, null, 0, 0, null, 0, null, null, None) == N.DDP_OK
+    assert lib.mx4_dequantize(2, null, null, 0, null, 0, None) == N.DDP_OK
+    assert lib.allreduce_mx4(1, 2, null, null, 0, 2, null, 0, None, None, 0, None) == N.DDP_OK
+    assert lib.allreduce_mx4_coded(1, 2, null, null, 0, 1, null, null, None, 0, None, None, 0, None) == N.DDP_OK
+
+
+# ----------------------------------------------------- tensor level ----
+
+class Gpu(torch.Tensor):
+    """A CPU tensor that says it lives on the GPU."""
+    is_cuda = True
+
+    def __getitem__(self, k):
+        return torch.Tensor._make_subclass(Gpu, torch.Tensor.__getitem__(self.as_subclass(torch.Tensor), k))
+
+
+def gpu(n, dtype=torch.uint8):
+    return torch.Tensor._make_subclass(Gpu, torch.zeros(n, dtype=dtype))
+
+
+def test_mx4_sizes():
+    x = ddp.Mx4(gpu(64), gpu(4), 100)
+    assert x.numel == 100
+    y = x.narrow(32, 68)
+    assert y.numel == 68 and y.codes.numel() == 48 and y.scales.numel() == 3
+    assert x.narrow(64, 0).numel == 0 and x.narrow(96, 4).codes.numel() == 16
+    for bad in ((1, 32), (32, 33), (0, 101), (-32, 64), (64, -32)):
+        with pytest.raises(ValueError):
+            x.narrow(*bad)
+    for codes, scales, n in ((gpu(63), gpu(4), 100), (gpu(64), gpu(3), 100), (gpu(64), gpu(4), 129),
+                             (torch.zeros(64, dtype=torch.uint8), gpu(4), 100), (gpu(128)[::2], gpu(4), 100)):
+        with pytest.raises(ValueError):
+            ddp.Mx4(codes, scales, n)
+    with pytest.raises(TypeError):
+        ddp.Mx4(gpu(64, torch.int8), gpu(4), 100)
+    with pytest.raises(ValueError):
+        ddp.Mx4.empty(-1, "cpu")
+
+
+def test_moments8_sizes():
+    ddp.Moments8([gpu(100), gpu(0)], [gpu(100), gpu(0)], [gpu(8), gpu(0)])
+    for m, v, s in (([gpu(100)], [gpu(99)], [gpu(8)]), ([gpu(100)], [gpu(100)], [gpu(4)]),
+                    ([gpu(100)], [gpu(100)] * 2, [gpu(8)]), ([], [], [])):
+        with pytest.raises(ValueError):
+            ddp.Moments8(m, v, s)
+    with pytest.raises(TypeError):
+        ddp.Moments8([gpu(100, torch.float32)], [gpu(100)], [gpu(8)])
+    with pytest.raises(ValueError):
+        ddp.Moments8.zeros([])
+
+
+def test_tensor_level_refusals():
+    row = ddp.Mx4(gpu(64), gpu(4), 100)
+    with pytest.raises(TypeError):
+        ddp.mx4_dequantize([gpu(64)])
+    with pytest.raises(ValueError):
+        ddp.mx4_dequantize([])
+    with pytest.raises(ValueError):
+        ddp.mx4_dequantize([row, ddp.Mx4(gpu(16), gpu(1), 20)])
+    with pytest.raises(ValueError):
+        ddp.allreduce_mx4([row] * 17)
+    row.codes.resize_(48)
+    with pytest.raises(ValueError):
+        ddp.mx4_dequantize([row])
+    mom = ddp.Moments8([gpu(100)], [gpu(100)], [gpu(8)])
+    mg = ddp.MultiGrad(gpu(100, torch.float32))
+    w = gpu(100, torch.float32)
+    with pytest.raises(TypeError):
+        mg.bind_adamw8(w, (gpu(100), gpu(100), gpu(8)))
+    with pytest.raises(ValueError):
+        ddp.MultiGrad(gpu(99, torch.float32)).bind_adamw8(gpu(99, torch.float32), mom)
+    run = mg.bind_adamw8(w, mom)
+    with pytest.raises(ValueError):
+        run(1e-3, 1, max_norm=1.0)
+    mom.scales[0].data = torch.zeros(8, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="bind it again"):
+        run(1e-3, 1)
