@@ -41,8 +41,14 @@ namespace {
 using rr::u32x2;
 using rr::u32x4;
 
-constexpr uint32_t kTileElems = 256;
+// Workgroups of 4 waves; a wave takes kSpans spans of 256 consecutive elements,
+// a lane 4 of each, 8 lanes a block.
+constexpr unsigned kLanes = 256;
+constexpr uint32_t kSpan = 256;
+constexpr int kSpans = 2;
+constexpr uint32_t kTileElems = 4 * kSpans * kSpan;
 constexpr uint32_t kBlockElems = DDP_MX_BLOCK;
+constexpr uint32_t kMaxGrid = 1u << 23;
 // Tensors (or pieces of them) per launch: as many as the arguments hold.
 constexpr int kCap = 120;
 
@@ -89,11 +95,6 @@ __device__ __forceinline__ uint32_t random_bits(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// What is added to a float32's bits below the 4 kept: 16 random bits and a
-// half, so that neither side is favoured by the rest that they leave out.
-__device__ __forceinline__ uint32_t low_bits(uint32_t r) { return ((r & 0xffffu) << 4) | 8u; }
-__device__ __forceinline__ uint32_t high_bits(uint32_t r) { return ((r >> 12) & 0xffff0u) | 8u; }
-
 __device__ __forceinline__ float decode_v(uint32_t code, float scale) {
     return __uint_as_float((code << 20) + (96u << 23)) * scale;
 }
@@ -111,33 +112,61 @@ __device__ __forceinline__ uint32_t scale_v(uint32_t top) {
     return e < 255u ? mx::larger(e, 32u) : 255u;
 }
 
-// up: 2^(127 - s), which brings the block's maximum to at most 448.
+// A moment's code is what a float32's exponent and top 3 bits of mantissa are
+// once its exponent starts where the code's does; the 20 bits below are the part
+// cut off, and 16 random bits and a half (neither side is favoured by the rest
+// that they leave out), added to them, carry into the code with its probability.
+// m, in scales (up = 2^(127 - s)) and times 2^-120, is subnormal just where its
+// code is: the code with the sign in front lies in the top byte.
 __device__ __forceinline__ uint32_t encode_m(float m, float up, uint32_t r) {
-    const float x = __builtin_fabsf(m) * up;
-    const uint32_t normal = ((__float_as_uint(x) + r) >> 20) - (120u << 3);
-    const uint32_t small = (static_cast<uint32_t>(__builtin_fminf(x, 0x1p-6f) * 0x1p29f) + r) >> 20;   // steps of 2^-9
-    return (x < 0x1p-6f ? small : normal) | ((__float_as_uint(m) >> 24) & 0x80u);
+#pragma clang fp contract(off)
+    const float x = __builtin_fabsf(m) * up * 0x1p-120f;
+    const uint32_t t = __float_as_uint(x) + ((r & 0xffffu) << 4) + 8u;
+    return (__float_as_uint(m) & 0x80000000u) | ((t << 4) & 0x7fffffffu);
 }
-__device__ __forceinline__ uint32_t encode_v(float v, uint32_t s, uint32_t r) {
-    const int32_t c = static_cast<int32_t>((__float_as_uint(v) + r) >> 20) - (static_cast<int32_t>(s - 31u) << 3);
-    return static_cast<uint32_t>(c < 0 ? 0 : c);
+// v less what its exponent starts at (`from`, and the half); below that code 0.
+__device__ __forceinline__ uint32_t encode_v(float v, uint32_t from, uint32_t r) {
+    const int32_t t = static_cast<int32_t>(__float_as_uint(v) + ((r >> 16) << 4) + from);
+    return static_cast<uint32_t>(t < 0 ? 0 : t) << 4;
+}
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t (&x)[4]) {
+    const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x0c0c0703u);
+    return __builtin_amdgcn_perm(x[3], x[2], 0x07030c0cu) | lo;
 }
 
-// Four bytes at any address, and those of them that lie in [0, n).
+// The weights' step, the root and the quotient by the hardware's instructions,
+// within 1 ulp each (correctly rounded ones take 40 instructions an element, and
+// this kernel would be bound by them: 230 us for 86.6M elements instead of 212):
+// beside moments of 3 bits that says nothing.  A second moment below 2^-126,
+// which those instructions take for zero, counts as that.
+__device__ __forceinline__ float step_weight(float w, float m, float v, const adamw::Factors& f) {
+#pragma clang fp contract(off)
+    const float least = __uint_as_float(mx::larger(__float_as_uint(v), 1u << 23));
+    const float d = __builtin_amdgcn_sqrtf(least) * f.root2 + f.eps;
+    const float q = m * __builtin_amdgcn_rcpf(d);
+    const float w0 = w * f.decay;
+    const float s = f.step_size * q;
+    return w0 - s;
+}
+
+// Four bytes at any address, those of them that lie in [0, n) unless WHOLE.
 typedef uint32_t __attribute__((aligned(1))) u32_any;
 typedef __attribute__((address_space(1))) const u32_any* GlobalIn1;
 typedef __attribute__((address_space(1))) u32_any* GlobalOut1;
-__device__ __forceinline__ uint32_t load_bytes(const char* p, int64_t i, int64_t n, bool whole) {
-    if (whole) return *(GlobalIn1)(p + i);
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t load_bytes(const char* p, int64_t i, int64_t n) {
+    if constexpr (WHOLE) return __builtin_nontemporal_load((GlobalIn1)(p + i));
     uint32_t x = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (i + e < n) x |= static_cast<uint32_t>(static_cast<uint8_t>(p[i + e])) << (8 * e);
     return x;
 }
-__device__ __forceinline__ void store_bytes(char* p, int64_t i, int64_t n, bool whole, uint32_t x) {
-    if (whole) {
-        *(GlobalOut1)(p + i) = x;
+template <bool WHOLE>
+__device__ __forceinline__ void store_bytes(char* p, int64_t i, int64_t n, uint32_t x) {
+    if constexpr (WHOLE) {
+        __builtin_nontemporal_store(x, (GlobalOut1)(p + i));
         return;
     }
 #pragma unroll
@@ -156,94 +185,130 @@ __device__ __forceinline__ int piece_of(A a, uint32_t tile) {
     return t;
 }
 
+// One tensor's streams.
+struct Streams {
+    const char* g;
+    char* w;
+    char* m;
+    char* v;
+    char* s;
+    char* p;
+    int64_t n;
+};
+// What a lane holds of a span.
+struct Lane {
+    u32x4 g, w;
+    uint32_t m, v, s;
+};
+
+template <bool GB, bool WHOLE>
+__device__ __forceinline__ Lane load_lane(const Streams& x, int64_t at) {
+    const int64_t i = at + mx::lane_id() * 4;
+    Lane l;
+    if constexpr (WHOLE) {
+        if constexpr (GB) {
+            const u32x2 h = gv::load2_nt(x.g + i * 2);
+            l.g = u32x4{h[0], h[1], 0u, 0u};
+        } else {
+            l.g = gv::load4_nt(x.g + i * 4);
+        }
+        l.w = gv::load4_nt(x.w + i * 4);
+    } else {
+        l.g = gv::load_some<GB, 4>(x.g, i, x.n);
+        l.w = gv::load_some<false, 4>(x.w, i, x.n);
+    }
+    l.m = load_bytes<WHOLE>(x.m, i, x.n);
+    l.v = load_bytes<WHOLE>(x.v, i, x.n);
+    const int64_t b = i / kBlockElems;
+    l.s = WHOLE || b * kBlockElems < x.n ? *reinterpret_cast<const uint16_t*>(x.s + b * 2) : 0u;
+    return l;
+}
+
+template <bool GB, int PM, bool WHOLE>
+__device__ __forceinline__ void step_lane(const Streams& x, int64_t at, const Lane& l, const adamw::Factors& f,
+                                          uint32_t key) {
+    const int64_t i = at + mx::lane_id() * 4;
+    const float ms = mx::scale_of(l.s & 0xffu);
+    const float vs = mx::scale_of(l.s >> 8);
+    const mx::f32x2 m01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(l.m, ms, false);
+    const mx::f32x2 m23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(l.m, ms, true);
+    float me[4] = {m01[0], m01[1], m23[0], m23[1]};
+    float ve[4], wn[4];
+    uint32_t mtop = 0, vtop = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        ve[e] = decode_v((l.v >> (8 * e)) & 0xffu, vs);
+        adamw::adamw_moments(rr::elem<GB>(l.g, e), me[e], ve[e], f);
+        wn[e] = step_weight(__uint_as_float(l.w[e]), me[e], ve[e], f);
+        if (WHOLE || i + e < x.n) {
+            mtop = mx::larger(mtop, __float_as_uint(me[e]) & 0x7fffffffu);
+            vtop = mx::larger(vtop, __float_as_uint(ve[e]));     // no sign, but for a NaN's
+        }
+    }
+    const uint32_t sm = scale_m(mx::max_of_8(mtop));
+    const uint32_t sv = scale_v(mx::max_of_8(vtop));
+    const float up = __uint_as_float((254u - (sm < 254u ? sm : 254u)) << 23);
+    const uint32_t from = 8u - ((sv - 31u) << 23);
+    const uint32_t x0 = key + static_cast<uint32_t>(i) * kGolden;
+    uint32_t mt[4], vt[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t r = random_bits(x0 + e * kGolden);
+        mt[e] = encode_m(me[e], up, r);
+        vt[e] = encode_v(ve[e], from, r);
+    }
+    const uint32_t mc = sm == 255u ? 0x7f7f7f7fu : top_bytes(mt);
+    const uint32_t vc = sv == 255u || sv == 0u ? 0u : top_bytes(vt);
+    store_bytes<WHOLE>(x.m, i, x.n, mc);
+    store_bytes<WHOLE>(x.v, i, x.n, vc);
+    const int64_t b = i / kBlockElems;
+    if ((threadIdx.x & 7) == 0 && (WHOLE || b * kBlockElems < x.n))
+        *reinterpret_cast<uint16_t*>(x.s + b * 2) = static_cast<uint16_t>(sm | sv << 8);
+    const u32x4 wq = {__float_as_uint(wn[0]), __float_as_uint(wn[1]), __float_as_uint(wn[2]), __float_as_uint(wn[3])};
+    const u32x2 h = {mx::pack_bf16(wn[0], wn[1]), mx::pack_bf16(wn[2], wn[3])};
+    if constexpr (WHOLE) {
+        gv::store4_nt(x.w + i * 4, wq);
+        if constexpr (PM == 1) gv::store4_nt(x.p + i * 4, wq);
+        if constexpr (PM == 2) gv::store2_nt(x.p + i * 2, h);
+    } else {
+        gv::store_some<false, 4>(x.w, i, x.n, wq);
+        if constexpr (PM == 1) gv::store_some<false, 4>(x.p, i, x.n, wq);
+        if constexpr (PM == 2) gv::store_some<true, 4>(x.p, i, x.n, u32x4{h[0], h[1], 0u, 0u});
+    }
+}
+
 // GB: bf16 gradients.  PM: the copy, 0 none, 1 float32, 2 bf16.
 template <bool GB, int PM>
-__global__ __launch_bounds__(mx::kWave) void adamw8_kernel(Adam8Args) {
+__global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args) {
     const KAdam8 a = (KAdam8)(__builtin_amdgcn_kernarg_segment_ptr());
     const uint32_t tiles = a->tiles;
     const adamw::KScalars k = (adamw::KScalars)(&a->scalars);
     const float norm = k->norm != nullptr ? gv::load_uniform(k->norm) : 0.0f;
     const int64_t step = k->step != nullptr ? gv::load_uniform(k->step) : k->host_step;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int t = piece_of(a, tile);
-        const char* const g = a->g[t];
-        char* const w = a->w[t];
-        char* const m = a->m[t];
-        char* const v = a->v[t];
-        char* const s = a->s[t];
-        char* const p = a->p[t];
-        const int64_t n = a->count[t];
-        const int64_t at = static_cast<int64_t>(tile - a->first_tile[t]) * kTileElems;
-        const int64_t i = at + threadIdx.x * 4;
-        const bool whole = at + kTileElems <= n || i + 4 <= n;
-        const bool held = i / kBlockElems * kBlockElems < n;
-        u32x4 gq, wq;
+        const Streams x = {a->g[t], a->w[t], a->m[t], a->v[t], a->s[t], a->p[t], a->count[t]};
+        const int64_t at = (static_cast<int64_t>(tile - a->first_tile[t]) * 4 + wave) * (kSpans * kSpan);
+        const bool whole = at + kSpans * kSpan <= x.n;
+        Lane l[kSpans];
         if (whole) {
-            if constexpr (GB) {
-                const u32x2 h = gv::load2_nt(g + i * 2);
-                gq = u32x4{h[0], h[1], 0u, 0u};
-            } else {
-                gq = gv::load4_nt(g + i * 4);
-            }
-            wq = gv::load4_nt(w + i * 4);
-        } else {
-            gq = gv::load_some<GB, 4>(g, i, n);
-            wq = gv::load_some<false, 4>(w, i, n);
+#pragma unroll
+            for (int u = 0; u < kSpans; ++u) l[u] = load_lane<GB, true>(x, at + u * kSpan);
         }
-        const uint32_t mq = load_bytes(m, i, n, whole);
-        const uint32_t vq = load_bytes(v, i, n, whole);
-        char* const sp = s + i / kBlockElems * 2;
-        const uint32_t sq = held ? *reinterpret_cast<const uint16_t*>(sp) : 0u;
+        // The factors (divisions, two powers) and the key while the data is in
+        // flight.
         adamw::Factors f;
         if (!adamw::factors(k, norm, step, f)) return;
         uint32_t key = mix_word(a->seed, static_cast<uint32_t>(step));
         key = mix_word(key, static_cast<uint32_t>(step >> 32));
         key = mix_word(mix_word(key, a->tensor[t]), a->piece[t]);
-        const uint32_t x0 = key + static_cast<uint32_t>(i) * kGolden;
-
-        const float ms = mx::scale_of(sq & 0xffu);
-        const float vs = mx::scale_of(sq >> 8);
-        const mx::f32x2 m01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mq, ms, false);
-        const mx::f32x2 m23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mq, ms, true);
-        float me[4] = {m01[0], m01[1], m23[0], m23[1]};
-        float ve[4], wn[4];
-        uint32_t mtop = 0, vtop = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            ve[e] = decode_v((vq >> (8 * e)) & 0xffu, vs);
-            wn[e] = __uint_as_float(wq[e]);
-            adamw::adamw_element(rr::elem<GB>(gq, e), wn[e], me[e], ve[e], f);
-            wq[e] = __float_as_uint(wn[e]);
-            if (i + e < n) {
-                mtop = mx::larger(mtop, __float_as_uint(me[e]) & 0x7fffffffu);
-                vtop = mx::larger(vtop, __float_as_uint(ve[e]) & 0x7fffffffu);
-            }
-        }
-        const uint32_t sm = scale_m(mx::max_of_8(mtop));
-        const uint32_t sv = scale_v(mx::max_of_8(vtop));
-        const float up = __uint_as_float((254u - (sm < 254u ? sm : 254u)) << 23);
-        uint32_t mc = 0, vc = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t r = random_bits(x0 + e * kGolden);
-            mc |= encode_m(me[e], up, low_bits(r)) << (8 * e);
-            vc |= encode_v(ve[e], sv, high_bits(r)) << (8 * e);
-        }
-        if (sm == 255u) mc = 0x7f7f7f7fu;
-        if (sv == 255u || sv == 0u) vc = 0u;
-        store_bytes(m, i, n, whole, mc);
-        store_bytes(v, i, n, whole, vc);
-        if (held && (threadIdx.x & 7) == 0) *reinterpret_cast<uint16_t*>(sp) = static_cast<uint16_t>(sm | sv << 8);
-        const u32x2 h = {rr::bf16_bits(wn[0]) | (rr::bf16_bits(wn[1]) << 16),
-                         rr::bf16_bits(wn[2]) | (rr::bf16_bits(wn[3]) << 16)};
         if (whole) {
-            gv::store4_nt(w + i * 4, wq);
-            if constexpr (PM == 1) gv::store4_nt(p + i * 4, wq);
-            if constexpr (PM == 2) gv::store2_nt(p + i * 2, h);
+#pragma unroll
+            for (int u = 0; u < kSpans; ++u) step_lane<GB, PM, true>(x, at + u * kSpan, l[u], f, key);
         } else {
-            gv::store_some<false, 4>(w, i, n, wq);
-            if constexpr (PM == 1) gv::store_some<false, 4>(p, i, n, wq);
-            if constexpr (PM == 2) gv::store_some<true, 4>(p, i, n, u32x4{h[0], h[1], 0u, 0u});
+            for (int64_t i = at; i < x.n && i < at + kSpans * kSpan; i += kSpan)
+                step_lane<GB, PM, false>(x, i, load_lane<GB, false>(x, i), f, key);
         }
     }
 }
@@ -261,6 +326,7 @@ const void* kernel_for(const AdamWLaunch& l) {
 }
 
 // The moments' values.
+constexpr int read_spans(bool bf16) { return bf16 ? 2 : 1; }
 struct Read8Args {
     const char* m[kCap];
     const char* v[kCap];
@@ -275,38 +341,68 @@ struct Read8Args {
 static_assert(sizeof(Read8Args) <= kArgBytes, "kernel arguments");
 typedef const __attribute__((address_space(4))) Read8Args* KRead8;
 
+// A lane's 8 elements of a span of 512 (mx.h: wide for float32 outputs).
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void load_moments(const char* m, const char* v, const char* s, int64_t at, int64_t n,
+                                             u32x2& mq, u32x2& vq, uint32_t& sq) {
+    const int64_t i = mx::first4<!BF16>(at), j = i + mx::second_after(!BF16);
+    mq = u32x2{load_bytes<WHOLE>(m, i, n), load_bytes<WHOLE>(m, j, n)};
+    vq = u32x2{load_bytes<WHOLE>(v, i, n), load_bytes<WHOLE>(v, j, n)};
+    const int64_t b = at / kBlockElems + mx::scale_place<!BF16>();
+    sq = WHOLE || b * kBlockElems < n ? *reinterpret_cast<const uint16_t*>(s + b * 2) : 0u;
+}
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void store_moments(char* m_out, char* v_out, int64_t at, int64_t n, u32x2 mq, u32x2 vq,
+                                              uint32_t sq) {
+    float m[8], v[8];
+    const mx::Scales s = mx::own_scales<!BF16>(sq);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float ms = mx::scale_of((h == 0 ? s.a : s.b) & 0xffu);
+        const float vs = mx::scale_of((h == 0 ? s.a : s.b) >> 8);
+        const mx::f32x2 m01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mq[h], ms, false);
+        const mx::f32x2 m23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mq[h], ms, true);
+        m[4 * h] = m01[0], m[4 * h + 1] = m01[1], m[4 * h + 2] = m23[0], m[4 * h + 3] = m23[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * h + e] = decode_v((vq[h] >> (8 * e)) & 0xffu, vs);
+    }
+    mx::store_values<BF16, !BF16, WHOLE>(m_out, at, n, m);
+    mx::store_values<BF16, !BF16, WHOLE>(v_out, at, n, v);
+}
+
 template <bool BF16>
-__global__ __launch_bounds__(mx::kWave) void adamw8_read_kernel(Read8Args) {
+__global__ __launch_bounds__(kLanes) void adamw8_read_kernel(Read8Args) {
+    constexpr int U = read_spans(BF16);
     const KRead8 a = (KRead8)(__builtin_amdgcn_kernarg_segment_ptr());
     const uint32_t tiles = a->tiles;
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int t = piece_of(a, tile);
+        const char* const m = a->m[t];
+        const char* const v = a->v[t];
+        const char* const s = a->s[t];
         const int64_t n = a->count[t];
-        const int64_t at = static_cast<int64_t>(tile - a->first_tile[t]) * kMxTileElems;
-        const int64_t i = at + threadIdx.x * 8;
-        if (i >= n) continue;
-        const bool whole = i + 8 <= n;
-        const char* const sp = a->s[t] + i / kBlockElems * 2;
-        const uint32_t sq = *reinterpret_cast<const uint16_t*>(sp);
-        float m[8], v[8];
+        const int64_t at = mx::wave_start<U>(tile - a->first_tile[t]);
+        u32x2 mq[U], vq[U];
+        uint32_t sq[U];
+        if (at + U * mx::kMxSpan <= n) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t mq = load_bytes(a->m[t], i + 4 * h, n, whole);
-            const uint32_t vq = load_bytes(a->v[t], i + 4 * h, n, whole);
-            const mx::f32x2 m01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mq, mx::scale_of(sq & 0xffu), false);
-            const mx::f32x2 m23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mq, mx::scale_of(sq & 0xffu), true);
-            m[4 * h] = m01[0], m[4 * h + 1] = m01[1], m[4 * h + 2] = m23[0], m[4 * h + 3] = m23[1];
+            for (int u = 0; u < U; ++u)
+                load_moments<BF16, true>(m, v, s, at + u * mx::kMxSpan, n, mq[u], vq[u], sq[u]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * h + e] = decode_v((vq >> (8 * e)) & 0xffu, mx::scale_of(sq >> 8));
+            for (int u = 0; u < U; ++u)
+                store_moments<BF16, true>(a->m_out[t], a->v_out[t], at + u * mx::kMxSpan, n, mq[u], vq[u], sq[u]);
+        } else {
+            for (int64_t i = at; i < n && i < at + U * mx::kMxSpan; i += mx::kMxSpan) {
+                load_moments<BF16, false>(m, v, s, i, n, mq[0], vq[0], sq[0]);
+                store_moments<BF16, false>(a->m_out[t], a->v_out[t], i, n, mq[0], vq[0], sq[0]);
+            }
         }
-        mx::store_oct<BF16>(a->m_out[t], i, n, whole, mx::pack_oct<BF16>(m));
-        mx::store_oct<BF16>(a->v_out[t], i, n, whole, mx::pack_oct<BF16>(v));
     }
 }
 
 int launch(const void* fn, void* args, uint32_t tiles, unsigned lds, void* stream, const char* what, const char** msg) {
     void* list[] = {args};
-    const hipError_t e = hipLaunchKernel(fn, dim3(std::min(tiles, kMaxWaveGrid)), dim3(mx::kWave), list, lds,
+    const hipError_t e = hipLaunchKernel(fn, dim3(std::min(tiles, kMaxGrid)), dim3(kLanes), list, lds,
                                          static_cast<hipStream_t>(stream));
     if (e == hipSuccess) return 0;
     *msg = what;
@@ -348,7 +444,7 @@ int launch_adamw8(const AdamW8Launch& l, const char** msg) {
         }
         if (a.n == 0) continue;
         a.tiles = static_cast<uint32_t>(tiles);
-        if (const int e = launch(fn, &a, a.tiles, 0, b.stream, "hipLaunchKernel(adamw8)", msg)) return e;
+        if (const int e = launch(fn, &a, a.tiles, lds_reserve(kAdamW8WgPerCu), b.stream, "hipLaunchKernel(adamw8)", msg)) return e;
     }
     return 0;
 }
@@ -371,7 +467,7 @@ int launch_adamw8_read(const Moments8Read& l, const char** msg) {
                 a.v_out[a.n] = static_cast<char*>(l.v_out[t]) + at * es;
                 a.count[a.n] = static_cast<uint32_t>(count);
                 a.first_tile[a.n] = static_cast<uint32_t>(tiles);
-                tiles += mx_tiles(count);
+                tiles += mx_tiles(count, read_spans(l.out_bf16));
                 at += count;
                 ++a.n;
             }
@@ -382,7 +478,7 @@ int launch_adamw8_read(const Moments8Read& l, const char** msg) {
         }
         if (a.n == 0) continue;
         a.tiles = static_cast<uint32_t>(tiles);
-        if (const int e = launch(fn, &a, a.tiles, 0, l.stream, "hipLaunchKernel(adamw8_read)", msg)) return e;
+        if (const int e = launch(fn, &a, a.tiles, lds_reserve(kMoments8WgPerCu), l.stream, "hipLaunchKernel(adamw8_read)", msg)) return e;
     }
     return 0;
 }

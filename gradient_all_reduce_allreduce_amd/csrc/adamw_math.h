@@ -85,7 +85,7 @@ struct Factors {
     float c, beta1, beta2, one_beta1, one_beta2, decay, eps, step_size, root2;
 };
 
-__device__ __forceinline__ void adamw_element(float g, float& w, float& m, float& v, const Factors& f) {
+__device__ __forceinline__ void adamw_moments(float g, float& m, float& v, const Factors& f) {
 #pragma clang fp contract(off)
     g = g * f.c;
     const float m0 = f.beta1 * m;
@@ -95,6 +95,11 @@ __device__ __forceinline__ void adamw_element(float g, float& w, float& m, float
     const float gg = g * g;
     const float v1 = f.one_beta2 * gg;
     v = v0 + v1;
+}
+
+__device__ __forceinline__ void adamw_element(float g, float& w, float& m, float& v, const Factors& f) {
+#pragma clang fp contract(off)
+    adamw_moments(g, m, v, f);
     const float r = __builtin_sqrtf(v) * f.root2;
     const float d = r + f.eps;
     const float q = m / d;

@@ -1791,8 +1791,8 @@ int mx4_reduce(ddp_reduce_op op, int32_t P, const uint8_t* const* codes, const u
     } else if ((s = check_rows(out, n_out, oes, "rank_out"))) {
         return s;
     }
-    const int64_t groups = ddp::mx4_reduce_workgroups(n);
-    const int64_t need = norm != nullptr ? norm_workspace(groups) : 0;
+    const int64_t partials = ddp::mx4_reduce_partials(n);
+    const int64_t need = norm != nullptr ? norm_workspace(partials) : 0;
     if (norm != nullptr && (s = check_workspace(workspace, workspace_bytes, need))) return s;
     // Coded rows may be written over the ones they came from: a block is read
     // from every rank before any is written.  Element sizes of 1 and 2 keep codes
@@ -1849,11 +1849,12 @@ int mx4_reduce(ddp_reduce_op op, int32_t P, const uint8_t* const* codes, const u
     l.left_type = left == nullptr ? 0 : (left_dtype == DDP_BF16 ? 2 : 1);
     if (norm != nullptr) {
         l.partials = static_cast<double*>(workspace);
-        if (groups > ddp::kNormFoldOver) l.zero = reinterpret_cast<uint64_t*>(l.partials + groups + ddp::kNormFold);
+        if (partials > ddp::kNormFoldOver) l.zero = reinterpret_cast<uint64_t*>(l.partials + partials + ddp::kNormFold);
     }
     l.stream = stream;
-    int e = ddp::launch_mx4_reduce(l, &msg);
-    if (e == 0 && norm != nullptr) e = ddp::launch_norm_of(l.partials, groups, l.partials + groups, norm, stream, &msg);
+    int64_t groups = 0;
+    int e = ddp::launch_mx4_reduce(l, &groups, &msg);
+    if (e == 0 && norm != nullptr) e = ddp::launch_norm_of(l.partials, groups, l.partials + partials, norm, stream, &msg);
     if (e != 0) return hip_fail(e, msg);
     return ok();
 }
@@ -1929,7 +1930,7 @@ int allreduce_mx4_coded(ddp_reduce_op op, int32_t P, const uint8_t* const* rank_
 int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes) {
     if (const int s = check_length(n, "n")) return s;
     if (bytes == nullptr) return fail(DDP_E_ARG, "bytes is NULL");
-    *bytes = norm_workspace(ddp::mx4_reduce_workgroups(n));
+    *bytes = norm_workspace(ddp::mx4_reduce_partials(n));
     return ok();
 }
 

@@ -9,9 +9,32 @@ namespace ddp {
 
 constexpr int64_t mx_blocks(int64_t n) { return n / DDP_MX_BLOCK + (n % DDP_MX_BLOCK != 0); }
 
-// Elements per one-wave workgroup of the 4-bit kernels: 8 per lane.
-constexpr int64_t kMxTileElems = 512;
-constexpr int64_t mx_tiles(int64_t n) { return n / kMxTileElems + (n % kMxTileElems != 0); }
+// The 4-bit kernels' workgroups: 4 waves, each taking so many spans of 512
+// elements.
+constexpr unsigned kMxLanes = 256;
+constexpr int64_t mx_tiles(int64_t n, int spans) { return (n + 2048 * spans - 1) / (2048 * spans); }
+// A grid holds fewer than 2^32 lanes; each workgroup walks on by its size.
+constexpr uint32_t kMaxMxGrid = 1u << 23;
+
+// Quantisation and reading back: spans per wave, and workgroups per CU (figures
+// in mx4.hip).
+constexpr int kMx4Spans = 2;
+constexpr int mx4_quantize_wg_per_cu(bool left) { return left ? 4 : 6; }
+constexpr int mx4_dequantize_wg_per_cu(bool bf16) { return bf16 ? 5 : 4; }
+
+// The all-reduce (figures in mx4_reduce.hip).  Spans per wave: two where a span
+// moves little, few ranks and no float32.
+constexpr int mx4_reduce_spans(int P, bool f32) { return !f32 && P <= 4 ? 2 : 1; }
+// Workgroups per CU where every rank receives values, 0 for no limit.
+constexpr int mx4_reduce_wg_per_cu(int P, bool f32, bool all_ranks, bool coded) {
+    if (!all_ranks || coded || P == 1) return 0;
+    if (f32) return P <= 3 ? 4 : P <= 6 ? 2 : 1;
+    return P <= 6 ? 4 : P <= 8 ? 3 : P <= 12 ? 2 : 1;
+}
+
+// The AdamW step with 8-bit moments and their reading back (adamw8.hip).
+constexpr int kAdamW8WgPerCu = 4;
+constexpr int kMoments8WgPerCu = 3;
 
 // P rows between values and codes.
 struct Mx4Launch {
@@ -45,9 +68,12 @@ struct Mx4Reduce {
     uint64_t* zero;                  // cleared by the first workgroup, or null
     void* stream;
 };
-int launch_mx4_reduce(const Mx4Reduce& l, const char** msg);
-// Workgroups of that launch, and so its partials.
-int64_t mx4_reduce_workgroups(int64_t n);
+// Also tells how many workgroups it started, and so partials it leaves.
+int launch_mx4_reduce(const Mx4Reduce& l, int64_t* workgroups, const char** msg);
+// Workgroups, and so partials, of such a launch at most.
+constexpr int64_t mx4_reduce_partials(int64_t n) {
+    return mx_tiles(n, 1) < kMaxMxGrid ? mx_tiles(n, 1) : static_cast<int64_t>(kMaxMxGrid);
+}
 
 // One AdamW step with 8-bit moments on n_tensors tensors.
 struct AdamW8Launch {

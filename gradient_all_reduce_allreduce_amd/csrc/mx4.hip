@@ -33,7 +33,35 @@ typedef const __attribute__((address_space(4))) Mx4Args* KMx4;
 
 // LEFT: the left-over, 0 none, 1 float32, 2 bf16.
 template <bool BF16, int LEFT>
-__global__ __launch_bounds__(mx::kWave) void mx4_quantize_kernel(Mx4Args) {
+constexpr bool kWide = !BF16 || LEFT == 1;
+
+template <bool BF16, int LEFT, bool WHOLE>
+__device__ __forceinline__ void quantize_span(const mx::Raw& g, const mx::Raw& r, char* left, char* codes, char* scales,
+                                              int64_t at, int64_t n) {
+    constexpr bool W = kWide<BF16, LEFT>;
+    float t[8];
+    mx::values_of<BF16, W>(g, t);
+    if constexpr (LEFT != 0) {
+        float x[8];
+        mx::values_of<LEFT == 2, W>(r, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] += x[e];
+    }
+    const mx::Coded q = mx::quantize8<W>(t);
+    mx::store_coded<W, WHOLE>(codes, scales, at, n, mx::shared_codes<W>(q.codes), q.scales);
+    if constexpr (LEFT != 0) {
+        float x[8];
+        mx::decode8(q.codes, q.scales, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = t[e] - x[e];
+        mx::store_values<LEFT == 2, W, WHOLE>(left, at, n, x, q.finite_a, q.finite_b);
+    }
+}
+
+template <bool BF16, int LEFT>
+__global__ __launch_bounds__(kMxLanes) void mx4_quantize_kernel(Mx4Args) {
+    constexpr bool W = kWide<BF16, LEFT>;
+    constexpr int U = kMx4Spans;
     const KMx4 a = (KMx4)(__builtin_amdgcn_kernarg_segment_ptr());
     const char* const in = a->values[blockIdx.y];
     char* const left = a->left[blockIdx.y];
@@ -42,37 +70,40 @@ __global__ __launch_bounds__(mx::kWave) void mx4_quantize_kernel(Mx4Args) {
     const int64_t n = a->n;
     const uint32_t tiles = a->tiles;
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t at = tile * kMxTileElems;
-        const int64_t i = at + threadIdx.x * 8;
-        const bool whole = at + kMxTileElems <= n || i + 8 <= n;
-        const mx::Oct<BF16> g = mx::load_oct<BF16>(in, i, n, whole);
-        float t[8];
-        mx::Oct<LEFT == 2> r;
-        if constexpr (LEFT != 0) r = mx::load_oct<LEFT == 2>(left, i, n, whole);
+        const int64_t at = mx::wave_start<U>(tile);
+        mx::Raw g[U], r[U];
+        if (at + U * mx::kMxSpan <= n) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t[e] = mx::oct_elem<BF16>(g, e);
-            if constexpr (LEFT != 0) t[e] += mx::oct_elem<LEFT == 2>(r, e);
-        }
-        const mx::Coded q = mx::quantize8(t);
-        if (i / DDP_MX_BLOCK * DDP_MX_BLOCK < n) {
-            mx::store_codes(codes, i, q.codes);
-            if ((threadIdx.x & 3) == 0) mx::store_scale(scales, i, q.scale);
-        }
-        if constexpr (LEFT != 0) {
-            if (q.finite) {
-                float x[8];
-                mx::decode8(q.codes, mx::scale_of(q.scale), x);
+            for (int u = 0; u < U; ++u) {
+                g[u] = mx::load_raw<BF16, W, true>(in, at + u * mx::kMxSpan, n);
+                if constexpr (LEFT != 0) r[u] = mx::load_raw<LEFT == 2, W, true>(left, at + u * mx::kMxSpan, n);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = t[e] - x[e];
-                mx::store_oct<LEFT == 2>(left, i, n, whole, mx::pack_oct<LEFT == 2>(x));
+            for (int u = 0; u < U; ++u)
+                quantize_span<BF16, LEFT, true>(g[u], r[u], left, codes, scales, at + u * mx::kMxSpan, n);
+        } else {
+            for (int64_t i = at; i < n; i += mx::kMxSpan) {
+                g[0] = mx::load_raw<BF16, W, false>(in, i, n);
+                if constexpr (LEFT != 0) r[0] = mx::load_raw<LEFT == 2, W, false>(left, i, n);
+                quantize_span<BF16, LEFT, false>(g[0], r[0], left, codes, scales, i, n);
             }
         }
     }
 }
 
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void dequantize_span(uint32_t c, uint32_t s, char* out, int64_t at, int64_t n,
+                                                mx::Exchange* lds) {
+    float x[8];
+    mx::decode8(c, mx::own_scales<false>(s), x);
+    if constexpr (!BF16) mx::exchange<true>(*lds, x);
+    mx::store_values<BF16, !BF16, WHOLE>(out, at, n, x);
+}
+
 template <bool BF16>
-__global__ __launch_bounds__(mx::kWave) void mx4_dequantize_kernel(Mx4Args) {
+__global__ __launch_bounds__(kMxLanes) void mx4_dequantize_kernel(Mx4Args) {
+    constexpr int U = kMx4Spans;
+    mx::Exchange* const lds = mx::exchange_area<!BF16>();
     const KMx4 a = (KMx4)(__builtin_amdgcn_kernarg_segment_ptr());
     char* const out = a->values[blockIdx.y];
     const char* const codes = a->codes[blockIdx.y];
@@ -80,17 +111,25 @@ __global__ __launch_bounds__(mx::kWave) void mx4_dequantize_kernel(Mx4Args) {
     const int64_t n = a->n;
     const uint32_t tiles = a->tiles;
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t at = tile * kMxTileElems;
-        const int64_t i = at + threadIdx.x * 8;
-        if (i >= n) continue;
-        float x[8];
-        mx::decode8(mx::load_codes(codes, i), mx::scale_of(mx::load_scale(scales, i)), x);
-        mx::store_oct<BF16>(out, i, n, at + kMxTileElems <= n || i + 8 <= n, mx::pack_oct<BF16>(x));
+        const int64_t at = mx::wave_start<U>(tile);
+        uint32_t c[U], s[U];
+        if (at + U * mx::kMxSpan <= n) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                c[u] = mx::load_codes<false, true>(codes, at + u * mx::kMxSpan, n);
+                s[u] = mx::load_scale<false, true>(scales, at + u * mx::kMxSpan, n);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) dequantize_span<BF16, true>(c[u], s[u], out, at + u * mx::kMxSpan, n, lds);
+        } else {
+            for (int64_t i = at; i < n; i += mx::kMxSpan)
+                dequantize_span<BF16, false>(mx::load_codes<false, false>(codes, i, n),
+                                             mx::load_scale<false, false>(scales, i, n), out, i, n, lds);
+        }
     }
 }
 
-int launch(const void* fn, const Mx4Launch& l, int wg_per_cu, const char* what, const char** msg) {
-    if (l.n == 0) return 0;
+int launch(const void* fn, const Mx4Launch& l, unsigned lds, const char* what, const char** msg) {
     Mx4Args a{};
     for (int r = 0; r < l.P; ++r) {
         a.values[r] = static_cast<char*>(const_cast<void*>(l.values[r]));
@@ -99,12 +138,11 @@ int launch(const void* fn, const Mx4Launch& l, int wg_per_cu, const char* what, 
         a.scales[r] = static_cast<char*>(l.scales[r]);
     }
     a.n = l.n;
-    a.tiles = static_cast<uint32_t>(mx_tiles(l.n));
-    // a grid holds fewer than 2^32 lanes
-    const unsigned grid = std::min(a.tiles, kMaxWaveGrid / static_cast<unsigned>(l.P));
+    a.tiles = static_cast<uint32_t>(mx_tiles(l.n, kMx4Spans));
+    const unsigned grid = std::min(a.tiles, kMaxMxGrid / static_cast<unsigned>(l.P));
     void* args[] = {&a};
-    const hipError_t e = hipLaunchKernel(fn, dim3(grid, static_cast<unsigned>(l.P)), dim3(mx::kWave), args,
-                                         lds_reserve(wg_per_cu), static_cast<hipStream_t>(l.stream));
+    const hipError_t e = hipLaunchKernel(fn, dim3(grid, static_cast<unsigned>(l.P)), dim3(kMxLanes), args, lds,
+                                         static_cast<hipStream_t>(l.stream));
     if (e == hipSuccess) return 0;
     *msg = what;
     return static_cast<int>(e);
@@ -120,13 +158,15 @@ int launch_mx4_quantize(const Mx4Launch& l, const char** msg) {
         {reinterpret_cast<const void*>(&mx4_quantize_kernel<true, 0>),
          reinterpret_cast<const void*>(&mx4_quantize_kernel<true, 1>),
          reinterpret_cast<const void*>(&mx4_quantize_kernel<true, 2>)}};
-    return launch(fns[l.bf16][l.left_type], l, 0, "hipLaunchKernel(mx4_quantize)", msg);
+    return launch(fns[l.bf16][l.left_type], l, lds_reserve(mx4_quantize_wg_per_cu(l.left_type != 0)),
+                  "hipLaunchKernel(mx4_quantize)", msg);
 }
 
 int launch_mx4_dequantize(const Mx4Launch& l, const char** msg) {
-    const void* const fns[2] = {reinterpret_cast<const void*>(&mx4_dequantize_kernel<false>),
-                                reinterpret_cast<const void*>(&mx4_dequantize_kernel<true>)};
-    return launch(fns[l.bf16], l, 0, "hipLaunchKernel(mx4_dequantize)", msg);
+    const void* const fn = l.bf16 ? reinterpret_cast<const void*>(&mx4_dequantize_kernel<true>)
+                                  : reinterpret_cast<const void*>(&mx4_dequantize_kernel<false>);
+    return launch(fn, l, lds_reserve(mx4_dequantize_wg_per_cu(l.bf16), l.bf16 ? 0 : mx::kExchangeBytes),
+                  "hipLaunchKernel(mx4_dequantize)", msg);
 }
 
 }  // namespace ddp

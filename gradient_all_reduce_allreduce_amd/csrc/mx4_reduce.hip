@@ -31,85 +31,138 @@ struct ReduceArgs {
     uint32_t tiles;
     int32_t n_out;
     int32_t mean;
-    int32_t left_type;
 };
 typedef const __attribute__((address_space(4))) ReduceArgs* KReduce;
 
-template <bool BF16>
-__device__ __forceinline__ void add_left(float (&g)[8], const char* left, int64_t i, int64_t n, bool whole) {
-    const mx::Oct<BF16> r = mx::load_oct<BF16>(left, i, n, whole);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] += mx::oct_elem<BF16>(r, e);
+// What a kernel writes: values, or codes with the left-over as the last
+// template argument has it.
+enum { kF32 = 0, kBf16 = 1, kCoded = 2, kCodedLeftF32 = 3, kCodedLeftBf16 = 4 };
+constexpr bool has_f32(int out) { return out == kF32 || out == kCodedLeftF32; }
+
+// s / P, correctly rounded.  For P no power of two by way of the float64
+// quotient, whose rounding to float32 is innocuous, and that from the product
+// with 1 / P and one correction by its remainder, which is exact in a fused
+// multiply-add (Markstein's division; a float64 division took 1.27 times as
+// long for 3 ranks).
+template <int P>
+__device__ __forceinline__ float mean_of(float s) {
+    if constexpr ((P & (P - 1)) == 0) {
+        return s * (1.0f / static_cast<float>(P));
+    } else {
+        constexpr double p = P, r = 1.0 / P;
+        const double x = s, q = x * r;
+        const double m = __builtin_fma(__builtin_fma(-p, q, x), r, q);
+        // a zero keeps its sign and an infinity is its own quotient, where the
+        // remainder would not know
+        constexpr int kOrdinary = 0x198;      // normal or subnormal, of either sign
+        return __builtin_amdgcn_classf(s, kOrdinary) ? static_cast<float>(m) : s;
+    }
 }
 
-// OUT: 0 float32, 1 bf16, 2 coded.
+template <int P, int OUT, bool WHOLE>
+__device__ __forceinline__ void reduce_span(KReduce a, const uint32_t (&c)[P], const uint32_t (&s)[P], const mx::Raw& left,
+                                            int64_t at, int64_t n, mx::Exchange* lds, double& sq) {
+    float g[8];
+    mx::decode8(c[0], mx::own_scales<false>(s[0]), g);
+#pragma unroll
+    for (int r = 1; r < P; ++r) {
+        float x[8];
+        mx::decode8(c[r], mx::own_scales<false>(s[r]), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] += x[e];
+    }
+    if (a->mean) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = mean_of<P>(g[e]);
+    }
+    if constexpr (OUT >= kCoded) {
+        float old[8];
+        if constexpr (OUT != kCoded) {
+            float (&x)[8] = old;
+            mx::values_of<OUT == kCodedLeftBf16, has_f32(OUT)>(left, x);
+            if constexpr (has_f32(OUT)) mx::exchange<false>(*lds, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] += x[e];
+        }
+        if constexpr (!WHOLE) {     // behind the row's end the codes are zero
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!mx::in_row<false>(at, n, e)) g[e] = 0.0f;
+        }
+        const mx::Coded q = mx::quantize8<false>(g);
+        float x[8];
+        mx::decode8(q.codes, q.scales, x);
+        for (int r = 0; r < a->n_out; ++r)
+            mx::store_coded<false, WHOLE>(a->out[r], a->out_scales[r], at, n, q.codes, q.scales);
+        if constexpr (OUT != kCoded) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = g[e] - x[e];
+            if constexpr (has_f32(OUT)) {
+                // a block without numbers keeps what it had
+                if (!q.finite_a) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = old[e];
+                }
+                mx::exchange<true>(*lds, y);
+                mx::store_values<false, true, WHOLE>(a->left, at, n, y);
+            } else {
+                mx::store_values<true, false, WHOLE>(a->left, at, n, y, q.finite_a);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = x[e];
+    } else {
+        if constexpr (has_f32(OUT)) mx::exchange<true>(*lds, g);
+        for (int r = 0; r < a->n_out; ++r) mx::store_values<OUT == kBf16, has_f32(OUT), WHOLE>(a->out[r], at, n, g);
+    }
+    if (a->partials != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (WHOLE || mx::in_row<OUT == kF32>(at, n, e)) sq = rr::square_to(sq, rr::written<OUT == kBf16>(g[e]));
+    }
+}
+
 template <int P, int OUT>
-__global__ __launch_bounds__(mx::kWave) void mx4_reduce_kernel(ReduceArgs) {
+__global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
+    constexpr int U = mx4_reduce_spans(P, has_f32(OUT));
+    mx::Exchange* const lds = mx::exchange_area<has_f32(OUT)>();
     const KReduce a = (KReduce)(__builtin_amdgcn_kernarg_segment_ptr());
     const int64_t n = a->n;
     const uint32_t tiles = a->tiles;
     double sq = 0.0;
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t at = tile * kMxTileElems;
-        const int64_t i = at + threadIdx.x * 8;
-        const bool whole = at + kMxTileElems <= n || i + 8 <= n;
-        const bool held = i / DDP_MX_BLOCK * DDP_MX_BLOCK < n;     // in a block of the row
-        uint32_t c[P], s[P];
+        const int64_t at = mx::wave_start<U>(tile);
+        uint32_t c[U][P], s[U][P];
+        mx::Raw left[U];
+        if (at + U * mx::kMxSpan <= n) {
 #pragma unroll
-        for (int r = 0; r < P; ++r) {
-            c[r] = held ? mx::load_codes(a->codes[r], i) : 0u;
-            s[r] = held ? mx::load_scale(a->scales[r], i) : 0u;
-        }
-        float g[8];
-        mx::decode8(c[0], mx::scale_of(s[0]), g);
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int r = 1; r < P; ++r) {
-            float x[8];
-            mx::decode8(c[r], mx::scale_of(s[r]), x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] += x[e];
-        }
-        if (a->mean) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = rr::mean_of<P>(g[e]);
-        }
-        if constexpr (OUT == 2) {
-            if (a->left_type == 1) add_left<false>(g, a->left, i, n, whole);
-            if (a->left_type == 2) add_left<true>(g, a->left, i, n, whole);
-            // behind the row's end the codes are zero
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = i + e < n ? g[e] : 0.0f;
-            const mx::Coded q = mx::quantize8(g);
-            float x[8];
-            mx::decode8(q.codes, mx::scale_of(q.scale), x);
-            if (held) {
-                for (int r = 0; r < a->n_out; ++r) {
-                    mx::store_codes(a->out[r], i, q.codes);
-                    if ((threadIdx.x & 3) == 0) mx::store_scale(a->out_scales[r], i, q.scale);
+                for (int r = 0; r < P; ++r) {
+                    c[u][r] = mx::load_codes<false, true>(a->codes[r], at + u * mx::kMxSpan, n);
+                    s[u][r] = mx::load_scale<false, true>(a->scales[r], at + u * mx::kMxSpan, n);
                 }
-            }
-            if (a->left_type != 0 && q.finite) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = g[e] - x[e];
-                if (a->left_type == 1) mx::store_oct<false>(a->left, i, n, whole, mx::pack_oct<false>(y));
-                if (a->left_type == 2) mx::store_oct<true>(a->left, i, n, whole, mx::pack_oct<true>(y));
+                if constexpr (OUT > kCoded)
+                    left[u] = mx::load_raw<OUT == kCodedLeftBf16, has_f32(OUT), true>(a->left, at + u * mx::kMxSpan, n);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = x[e];
+            for (int u = 0; u < U; ++u) reduce_span<P, OUT, true>(a, c[u], s[u], left[u], at + u * mx::kMxSpan, n, lds, sq);
         } else {
-            const mx::Oct<OUT == 1> o = mx::pack_oct<OUT == 1>(g);
-            for (int r = 0; r < a->n_out; ++r) mx::store_oct<OUT == 1>(a->out[r], i, n, whole, o);
-        }
-        if (a->partials != nullptr) {
+            for (int64_t i = at; i < n; i += mx::kMxSpan) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e < n) sq = rr::square_to(sq, rr::written<OUT == 1>(g[e]));
+                for (int r = 0; r < P; ++r) {
+                    c[0][r] = mx::load_codes<false, false>(a->codes[r], i, n);
+                    s[0][r] = mx::load_scale<false, false>(a->scales[r], i, n);
+                }
+                if constexpr (OUT > kCoded) left[0] = mx::load_raw<OUT == kCodedLeftBf16, has_f32(OUT), false>(a->left, i, n);
+                reduce_span<P, OUT, false>(a, c[0], s[0], left[0], i, n, lds, sq);
+            }
         }
     }
     if (a->partials != nullptr) {
-        sq = gv::wave_sum63(sq);
-        if (threadIdx.x == 63) {
+        sq = gv::block_sum<kMxLanes>(sq);
+        if (threadIdx.x == 0) {
             a->partials[blockIdx.x] = sq;
             if (blockIdx.x == 0 && a->zero != nullptr) *a->zero = 0;
         }
@@ -132,11 +185,17 @@ const void* kernel_for(int P) {
     }
 }
 
+// LDS that lets so many workgroups share a CU, beside what the kernel has of its
+// own (the exchange, and the norm's four sums).
+unsigned lds_for(int wg_per_cu, bool f32) {
+    const unsigned own = (f32 ? mx::kExchangeBytes : 0) + (kMxLanes / 64) * sizeof(double);
+    if (wg_per_cu == 1) return kLdsBytesPerCu / 2;      // with its own, more than half
+    return lds_reserve(wg_per_cu, own);
+}
+
 }  // namespace
 
-int64_t mx4_reduce_workgroups(int64_t n) { return std::min<int64_t>(mx_tiles(n), kMaxWaveGrid); }
-
-int launch_mx4_reduce(const Mx4Reduce& l, const char** msg) {
+int launch_mx4_reduce(const Mx4Reduce& l, int64_t* workgroups, const char** msg) {
     ReduceArgs a{};
     for (int r = 0; r < l.P; ++r) {
         a.codes[r] = static_cast<const char*>(l.codes[r]);
@@ -146,18 +205,25 @@ int launch_mx4_reduce(const Mx4Reduce& l, const char** msg) {
         a.out[r] = static_cast<char*>(l.out[r]);
         a.out_scales[r] = static_cast<char*>(l.out_scales[r]);
     }
+    const bool coded = l.out_type == kCoded;
+    const int out = l.out_type + (coded ? l.left_type : 0);
+    const bool f32 = has_f32(out);
     a.left = static_cast<char*>(l.left);
     a.partials = l.partials;
     a.zero = l.zero;
     a.n = l.n;
-    a.tiles = static_cast<uint32_t>(mx_tiles(l.n));
+    a.tiles = static_cast<uint32_t>(mx_tiles(l.n, mx4_reduce_spans(l.P, f32)));
     a.n_out = l.n_out;
     a.mean = l.mean;
-    a.left_type = l.left_type;
-    const void* fn = l.out_type == 0 ? kernel_for<0>(l.P) : l.out_type == 1 ? kernel_for<1>(l.P) : kernel_for<2>(l.P);
+    const void* fn = out == kF32 ? kernel_for<kF32>(l.P) : out == kBf16 ? kernel_for<kBf16>(l.P)
+                     : out == kCoded ? kernel_for<kCoded>(l.P)
+                     : out == kCodedLeftF32 ? kernel_for<kCodedLeftF32>(l.P) : kernel_for<kCodedLeftBf16>(l.P);
+    const unsigned grid = std::min(a.tiles, kMaxMxGrid);
+    *workgroups = grid;
     void* args[] = {&a};
-    const hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(mx4_reduce_workgroups(l.n))), dim3(mx::kWave),
-                                         args, 0, static_cast<hipStream_t>(l.stream));
+    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kMxLanes), args,
+                                         lds_for(mx4_reduce_wg_per_cu(l.P, f32, l.n_out > 1, coded), f32),
+                                         static_cast<hipStream_t>(l.stream));
     if (e == hipSuccess) return 0;
     *msg = "hipLaunchKernel(mx4_reduce)";
     return static_cast<int>(e);

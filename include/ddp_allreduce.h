@@ -1068,7 +1068,7 @@ int allreduce_mx4_coded(ddp_reduce_op op, int32_t P, const uint8_t* const* rank_
 
 /*
  * allreduce_mx4_workspace_bytes -- host only: the workspace of the two calls
- * above when they leave a norm, in *bytes (8 for each 512 elements, and some).
+ * above when they leave a norm, in *bytes (8 for each 2,048 elements, and some).
  * Errors: DDP_E_ARG.
  */
 int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes);

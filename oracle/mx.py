@@ -22,7 +22,7 @@ probabilities and the mean of a long run.
 
 import numpy as np
 
-from .grads import adamw
+from .grads import _power, adamw
 
 BLOCK = 32
 LEVELS = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
@@ -125,14 +125,15 @@ def moments_decode(m, v, scales):
 
 def _round_at_random(x, values, r):
     """Codes of x >= 0, in scales: the code below, or the next one if the part
-    cut off (20 bits of it) and 16 random bits and a half reach a whole."""
+    cut off (20 bits of it, the nearest where m's steps are equal, all that a
+    float32 has elsewhere) and 16 random bits and a half reach a whole."""
     low = np.clip(np.searchsorted(values, x, side="right") - 1, 0, None)
     high = np.minimum(low + 1, values.size - 1)
     gap = values[high] - values[low]
     with np.errstate(all="ignore"):
         part = np.where(gap > 0, (x - values[low]) / np.where(gap > 0, gap, 1), 0)
     part = np.clip(part, 0, None)          # below the least code: that code
-    return np.where(np.floor(part * 2 ** 20) + 16 * r + 8 >= 2 ** 20, high, low)
+    return np.where(np.rint(part * 2 ** 20) + 16 * r + 8 >= 2 ** 20, high, low)
 
 
 def moments_encode(m, v, bits):
@@ -185,7 +186,32 @@ def random_bits(n, seed, step, tensor, first=0):
 
 
 def adamw8(g, w, m, v, scales, c, lr, b1, b2, eps, wd, t, seed, tensor):
-    """One step on one tensor as the kernel takes it: (w, m, v, scales)."""
+    """One step on one tensor: (w, m, v, scales).  The codes are what the kernel
+    writes; the weights' root and quotient are rounded correctly here and within
+    1 ulp each there, see weight_bound."""
     mv, vv = moments_decode(m, v, scales)
-    w, mv, vv = adamw(g, w, mv, vv, c, lr, b1, b2, eps, wd, t)
+    f = np.float32
+    _, mv, vv = adamw(g, w, mv, vv, c, lr, b1, b2, eps, wd, t)
+    with np.errstate(all="ignore"):
+        least = np.maximum(vv, f(2.0 ** -126))
+        w = np.asarray(w, f) * f(1.0 - lr * wd) - _update(mv, least, lr, b1, b2, eps, t)
     return (w, *moments_encode(mv, vv, random_bits(m.size, seed, t, tensor)))
+
+
+def _update(m, v, lr, b1, b2, eps, t):
+    f = np.float32
+    return f(lr / (1.0 - _power(b1, t))) * (m / (np.sqrt(v) * f(1.0 / np.sqrt(1.0 - _power(b2, t))) + f(eps)))
+
+
+def weight_bound(g, w, m, v, scales, c, lr, b1, b2, eps, wd, t):
+    """How far the kernel's new weights may be from adamw8's.  Relative errors in
+    steps of 2^-24 of the quotient: here root, product, sum and quotient 1 each;
+    there root 2, product 1, sum 1, reciprocal 2, product 1: 11 together.  Then on
+    both sides the product with the step's size, 1 each, and the difference, 1
+    each of the weight; products of these errors and of subnormal results are
+    covered by one more of each."""
+    mv, vv = moments_decode(m, v, scales)
+    new, mv, vv = adamw(g, w, mv, vv, c, lr, b1, b2, eps, wd, t)
+    with np.errstate(all="ignore"):
+        u = np.abs(_update(mv, np.maximum(vv, np.float32(2.0 ** -126)), lr, b1, b2, eps, t).astype(np.float64))
+        return 2.0 ** -24 * (14 * u + 3 * (np.abs(w.astype(np.float64)) + u)) + 2.0 ** -126

@@ -43,7 +43,7 @@ def dequantize_args(**change):
 
 def reduce_args(**change):
     a = dict(op="mean", P=2, rank_codes=[at(4), at(5)], rank_scales=[at(6), at(7)], n=1000, rank_out=[at(0), at(1)],
-             out_dtype=ddp.F32, norm=NORM, workspace=WS, workspace_bytes=16)
+             out_dtype=ddp.F32, norm=NORM, workspace=WS, workspace_bytes=8)
     a.update(change)
     return a
 
@@ -51,7 +51,7 @@ def reduce_args(**change):
 def coded_args(**change):
     a = dict(op="mean", P=2, rank_codes=[at(4), at(5)], rank_scales=[at(6), at(7)], n=1000, out_codes=[at(8), at(9)],
              out_scales=[at(10), at(11)], residual=at(2), residual_dtype=ddp.F32, norm=NORM, workspace=WS,
-             workspace_bytes=16)
+             workspace_bytes=8)
     a.update(change)
     return a
 
@@ -118,9 +118,9 @@ NORMS = [
     (dict(op=2), N.DDP_E_ARG, None),
     (dict(norm=NORM + 2), N.DDP_E_ALIGN, "norm"),
     (dict(workspace=None), N.DDP_E_ARG, "workspace"),
-    (dict(workspace_bytes=15), N.DDP_E_ARG, "workspace"),
+    (dict(workspace_bytes=7), N.DDP_E_ARG, "workspace"),
     (dict(workspace=WS + 8), N.DDP_E_ALIGN, "workspace"),
-    (dict(norm=WS + 12), N.DDP_E_OVERLAP, None),
+    (dict(norm=WS + 4), N.DDP_E_OVERLAP, None),
     (dict(norm=at(4, 16)), N.DDP_E_OVERLAP, None),
     (dict(workspace=at(6, 16)), N.DDP_E_OVERLAP, None),
 ]
@@ -225,11 +225,11 @@ def test_read_refusals(change, status, text):
 def test_workspace():
     assert ddp.allreduce_mx4_workspace_bytes(0) == 0
     assert ddp.allreduce_mx4_workspace_bytes(1) == 8
-    assert ddp.allreduce_mx4_workspace_bytes(513) == 16
-    with pytest.raises(DdpError):
-        ddp.allreduce_mx4_workspace_bytes(-1)
-    with pytest.raises(DdpError):
-        ddp.allreduce_mx4_workspace_bytes((1 << 40) + 1)
+    assert ddp.allreduce_mx4_workspace_bytes(2049) == 16
+    assert ddp.allreduce_mx4_workspace_bytes(1 << 40) <= 1 << 27
+    for n in (-1, (1 << 40) + 1):
+        with pytest.raises(DdpError):
+            ddp.allreduce_mx4_workspace_bytes(n)
     assert N.lib().allreduce_mx4_workspace_bytes(5, None) == N.DDP_E_ARG
 
 
