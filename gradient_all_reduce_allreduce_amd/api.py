@@ -1090,10 +1090,12 @@ class MultiGrad:
         same bits, and replicas that are to stay identical need the same
         seed."""
         bound = self._state8(w, moments, params)
-        check = _unmoved(self._held, *(x for x in bound if x is not None))
+        check = _unmoved(self._held, *(x for x in (bound[0], bound[-1]) if x is not None))
+        kept = moments._kept
 
         def run(lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=None, seed=0):
             check()
+            kept.check()
             self._adamw(bound, lr, step, betas, eps, weight_decay, norm, max_norm, seed)
 
         run.tensors = (self.grads, *(x.tensors if x is not None else None for x in bound))
@@ -1107,7 +1109,7 @@ class MultiGrad:
         m, v, scales = moments._held
         if m.numels != self._held.numels or moments.device != self.device:
             raise ValueError("adamw8: need moments of each gradient's size on its device")
-        moments._check()
+        moments._kept.check()
         w, _, _, params = self._state(w, None, None, params)
         return w, m, v, scales, params
 
@@ -1177,30 +1179,61 @@ def adamw_step(grads, w, m, v, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_de
     mg._adamw(mg._state(w, m, v, params), lr, step, betas, eps, weight_decay, norm, max_norm)
 
 
+class _Kept:
+    """Storages of tensors that an object keeps to itself, so that nothing but
+    a resize of the storage can take their memory away: ``check()`` refuses that,
+    at 0.2 us of host time per storage."""
+
+    def __init__(self, tensors, what):
+        storages = {}
+        for t in tensors:
+            st = t.untyped_storage()
+            storages.setdefault(st.data_ptr(), st)
+        self.what, self.storages = what, list(storages.values())
+        self.at = [(st.data_ptr(), st.nbytes()) for st in self.storages]
+
+    def check(self):
+        if [(st.data_ptr(), st.nbytes()) for st in self.storages] != self.at:
+            raise ValueError(f"{self.what}: the memory was resized since it was bound")
+
+
 class Moments8:
     """The two moments of AdamW in 8 bits: for each tensor ``m`` and ``v``, a
     byte per element, and ``scales``, two bytes per block of 32 elements (lists
     of contiguous uint8 GPU tensors; adamw8_step_multi in the C header has the
-    formats).  They are what a checkpoint keeps; ``Moments8(m, v, scales)``
-    makes them usable again, and ``Moments8.zeros`` new ones.  The tensors are
-    checked and their addresses taken once, and a tensor that is given other
-    memory or another size afterwards is refused."""
+    formats).  They are what a checkpoint keeps; ``Moments8(m, v, scales)`` makes
+    them usable again, and ``Moments8.zeros`` new ones.  The object keeps the
+    memory that the tensors have when it is made: values go in by ``copy_`` to
+    them or to ``m``, ``v`` and ``scales`` of the object, and a tensor that is
+    given other memory is no longer a part of it."""
 
     def __init__(self, m, v, scales):
         import torch
         held = []
         for x, what in ((m, "m"), (v, "v"), (scales, "scales")):
-            x = _tensor_list(x, f"Moments8 {what}", (torch.uint8,))
+            x = [t.detach() for t in _tensor_list(x, f"Moments8 {what}", (torch.uint8,))]
             held.append(_Held(x, f"Moments8 {what}", [t.numel() for t in x]))
         numels = held[0].numels
         if held[1].numels != numels or held[2].numels != [2 * (-(-n // MX_BLOCK)) for n in numels]:
             raise ValueError("Moments8: need a byte of m and of v per element and two scale bytes per block of 32")
-        self.m, self.v, self.scales = (list(h.tensors) for h in held)
-        self.device = self.m[0].device
+        self.device = held[0].tensors[0].device
         if any(h.tensors[0].device != self.device for h in held):
             raise ValueError("Moments8: every tensor must live on the same GPU")
-        self._held = held
-        self._check = _unmoved(*held)
+        self._held, self.numels = held, numels
+        self._kept = _Kept(sum((h.tensors for h in held), ()), "Moments8")
+        self._list = (len(numels), _long_array(numels), *(h.ptrs for h in held))
+
+    @property
+    def m(self):
+        return [t.detach() for t in self._held[0].tensors]
+
+    @property
+    def v(self):
+        return [t.detach() for t in self._held[1].tensors]
+
+    @property
+    def scales(self):
+        return [t.detach() for t in self._held[2].tensors]
 
     @classmethod
     def zeros(cls, tensors):
@@ -1222,13 +1255,13 @@ class Moments8:
         """Returns ``run()``, which writes the moments' values to ``m_out`` and
         ``v_out`` (one tensor of each size, all float32 or all bfloat16)."""
         bound = self._outputs(m_out, v_out)
-        check = _unmoved(*self._held, *bound)
+        check = _unmoved(*bound)
 
         def run():
             check()
             self._read(bound)
 
-        run.tensors = (self.m, self.v, self.scales, *(x.tensors for x in bound))
+        run.tensors = tuple(x.tensors for x in bound)
         return run
 
     def _outputs(self, m_out, v_out):
@@ -1236,9 +1269,9 @@ class Moments8:
         bound = []
         for x, what in ((m_out, "m_out"), (v_out, "v_out")):
             x = _tensor_list(x, f"Moments8 {what}", (torch.float32, torch.bfloat16))
-            if [t.numel() for t in x] != self._held[0].numels or x[0].device != self.device:
+            if [t.numel() for t in x] != self.numels or x[0].device != self.device:
                 raise ValueError(f"Moments8 {what}: need one tensor of each moment's size on its device")
-            bound.append(_Held(x, f"Moments8 {what}", self._held[0].numels))
+            bound.append(_Held(x, f"Moments8 {what}", self.numels))
         if len({t.dtype for h in bound for t in h.tensors}) > 1:
             raise ValueError("Moments8: outputs must all have the same element type")
         return bound
@@ -1247,8 +1280,7 @@ class Moments8:
         """The moments' values as new tensors (default float32): (list of m,
         list of v)."""
         import torch
-        self._check()
-        m, v = ([torch.empty(n, dtype=dtype or torch.float32, device=self.device) for n in self._held[0].numels]
+        m, v = ([torch.empty(n, dtype=dtype or torch.float32, device=self.device) for n in self.numels]
                 for _ in range(2))
         self._read(self._outputs(m, v))
         return m, v
@@ -1258,10 +1290,9 @@ class Moments8:
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device.index):
                 return self._read(bound)
-        m, v, scales = self._held
-        _check(N.lib().adamw8_read_multi(len(m.numels), _long_array(m.numels), m.ptrs, v.ptrs, scales.ptrs,
-                                         bound[0].ptrs, bound[1].ptrs, torch_dtype_code(bound[0].tensors[0].dtype),
-                                         _raw_stream(self.device.index)))
+        self._kept.check()
+        _check(N.lib().adamw8_read_multi(*self._list, bound[0].ptrs, bound[1].ptrs,
+                                         torch_dtype_code(bound[0].tensors[0].dtype), _raw_stream(self.device.index)))
 
 
 def adamw8_step(grads, w, moments, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params=None, norm=None,

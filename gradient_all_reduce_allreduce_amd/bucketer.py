@@ -112,7 +112,7 @@ class GradBucketer:
         ``x.narrow(b * bucket_elems, bucket_len(b))`` when buckets are a
         multiple of 32 elements)."""
         from .mx4 import Mx4
-        return [Mx4.empty(self.total, self.device) for _ in range(P)]
+        return Mx4.rows(P, self.total, self.device)
 
     def bucket_view(self, arena_row, b):
         """Bucket b of one rank's arena row (its live elements only)."""

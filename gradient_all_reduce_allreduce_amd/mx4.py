@@ -23,7 +23,11 @@ def _blocks(numel):
 class Mx4:
     """One rank's coded gradient of ``numel`` elements: ``codes``, 16 bytes per
     block of 32 elements, on a 16-byte line, and ``scales``, a byte per block
-    (contiguous uint8 GPU tensors)."""
+    (contiguous uint8 GPU tensors).  The object keeps the memory that they have
+    when it is made; a tensor that is given other memory is no longer a part of
+    it."""
+
+    __slots__ = ("numel", "device", "_parts", "_kept", "codes_at", "scales_at")
 
     def __init__(self, codes, scales, numel):
         import torch
@@ -36,21 +40,44 @@ class Mx4:
                 raise ValueError(f"Mx4: {what} must be contiguous and hold {size} bytes for {numel} elements")
         if codes.device != scales.device:
             raise ValueError("Mx4: codes and scales must live on the same GPU")
-        self.codes, self.scales, self.numel = codes, scales, int(numel)
+        codes, scales = codes.detach().view(-1), scales.detach().view(-1)
+        self._set(int(numel), codes, 0, scales, 0, api._Kept((codes, scales), "Mx4"))
+
+    def _set(self, numel, codes, codes_from, scales, scales_from, kept):
+        self.numel, self.device, self._kept = numel, codes.device, kept
+        self._parts = (codes, codes_from, scales, scales_from)
+        self.codes_at = codes.data_ptr() + codes_from
+        self.scales_at = scales.data_ptr() + scales_from
+        return self
+
+    @classmethod
+    def rows(cls, P, numel, device="cuda"):
+        """Room for P rows of ``numel`` elements in one allocation, each on a
+        4 KiB line and no two a power of two apart: a list of P Mx4."""
+        import torch
+        if numel < 0:
+            raise ValueError(f"Mx4: numel = {numel} is negative")
+        blocks = _blocks(numel)
+        stride = -(-17 * blocks // 4096) * 4096 + 4096
+        memory = torch.empty(P * stride, dtype=torch.uint8, device=device)
+        kept = api._Kept((memory,), "Mx4")
+        return [cls.__new__(cls)._set(numel, memory, r * stride, memory, r * stride + 16 * blocks, kept)
+                for r in range(P)]
 
     @classmethod
     def empty(cls, numel, device="cuda"):
         """Room for ``numel`` elements."""
-        import torch
-        if numel < 0:
-            raise ValueError(f"Mx4.empty: numel = {numel} is negative")
-        blocks = _blocks(numel)
-        both = torch.empty(17 * blocks, dtype=torch.uint8, device=device)
-        return cls(both[:16 * blocks], both[16 * blocks:], numel)
+        return cls.rows(1, numel, device)[0]
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        x, at = self._parts[:2]
+        return x[at:at + 16 * _blocks(self.numel)]
+
+    @property
+    def scales(self):
+        x, at = self._parts[2:]
+        return x[at:at + _blocks(self.numel)]
 
     def narrow(self, start, length):
         """The elements ``start`` .. ``start + length - 1`` as an Mx4 in the
@@ -60,8 +87,9 @@ class Mx4:
             raise ValueError(f"Mx4.narrow: elements {start} to {start + length} of {self.numel}")
         if start % BLOCK or (length % BLOCK and start + length != self.numel):
             raise ValueError("Mx4.narrow: must begin and end at blocks of 32 elements")
-        b, k = start // BLOCK, _blocks(length)
-        return Mx4(self.codes[16 * b:16 * (b + k)], self.scales[b:b + k], length)
+        b = start // BLOCK
+        codes, c, scales, s = self._parts
+        return Mx4.__new__(Mx4)._set(length, codes, c + 16 * b, scales, s + b, self._kept)
 
 
 def _coded_rows(coded, what):
@@ -69,16 +97,23 @@ def _coded_rows(coded, what):
     coded = list(coded)
     if not 1 <= len(coded) <= api.MAX_RANKS:
         raise ValueError(f"{what}: need 1..{api.MAX_RANKS} coded rows, got {len(coded)}")
+    kept = None
     for c in coded:
         if not isinstance(c, Mx4):
             raise TypeError(f"{what}: {type(c).__name__} where an Mx4 is needed")
-    n, index, blocks = coded[0].numel, coded[0].codes.get_device(), _blocks(coded[0].numel)
-    for c in coded:
-        if c.numel != n or c.codes.get_device() != index:
+        if c.numel != coded[0].numel or c.device != coded[0].device:
             raise ValueError(f"{what}: every row needs the same device and size")
-        if c.codes.numel() != 16 * blocks or c.scales.numel() != blocks:
-            raise ValueError(f"{what}: a row's tensors were given another size")
-    return coded, [c.codes.data_ptr() for c in coded], [c.scales.data_ptr() for c in coded]
+        if c._kept is not kept:
+            kept = c._kept
+            kept.check()
+    return coded, [c.codes_at for c in coded], [c.scales_at for c in coded]
+
+
+def _new_rows(P, n, dtype, device):
+    """P tensors of n elements in one allocation, each on a 4 KiB line."""
+    import torch
+    line = 4096 // (2 if dtype == torch.bfloat16 else 4)
+    return list(torch.empty(P, -(-n // line) * line + line, dtype=dtype, device=device)[:, :n].unbind(0))
 
 
 def _residual_tensors(residual, like, what):
@@ -106,10 +141,8 @@ def mx4_quantize(tensors, residual=None, out=None):
     if residual is not None:
         residual = _residual_tensors(residual, tensors, "mx4_quantize")
         left, lcode = [t.data_ptr() for t in residual], api.torch_dtype_code(residual[0].dtype)
-    if out is None:
-        out = [Mx4.empty(n, x.device) for _ in tensors]
-    out, codes, scales = _coded_rows(out, "mx4_quantize out")
-    if len(out) != len(tensors) or out[0].numel != n or out[0].codes.get_device() != index:
+    out, codes, scales = _coded_rows(out if out is not None else Mx4.rows(len(tensors), n, x.device), "mx4_quantize out")
+    if len(out) != len(tensors) or out[0].numel != n or out[0].device != x.device:
         raise ValueError("mx4_quantize: out must match the gradients, one Mx4 per rank")
     api.mx4_quantize_rows(len(tensors), [t.data_ptr() for t in tensors], api.torch_dtype_code(x.dtype), n, left, lcode,
                           codes, scales, api._raw_stream(index))
@@ -125,9 +158,8 @@ def mx4_dequantize(coded, out=None, dtype=None):
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
             return mx4_dequantize(coded, out, dtype)
-    if out is None:
-        out = [torch.empty(n, dtype=dtype or torch.float32, device=device) for _ in coded]
-    out = api._rank_tensors(out, "mx4_dequantize out")
+    out = api._rank_tensors(out, "mx4_dequantize out") if out is not None \
+        else _new_rows(len(coded), n, dtype or torch.float32, device)
     if len(out) != len(coded) or out[0].numel() != n or out[0].get_device() != device.index:
         raise ValueError("mx4_dequantize: out must match the coded rows, one tensor per rank")
     api.mx4_dequantize_rows(len(coded), codes, scales, n, [t.data_ptr() for t in out],
@@ -161,13 +193,11 @@ def _allreduce(coded, op, out, out_dtype, residual, with_norm):
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             return _allreduce(coded, op, out, out_dtype, residual, with_norm)
-    if out is None:
-        out = [torch.empty(n, dtype=out_dtype or torch.float32, device=device) for _ in range(P)]
-    out = list(out)
+    out = list(out) if out is not None else _new_rows(P, n, out_dtype or torch.float32, device)
     again = bool(out) and isinstance(out[0], Mx4)
     if again:
         out, out_codes, out_scales = _coded_rows(out, "allreduce_mx4 out")
-        size, where = out[0].numel, out[0].codes.get_device()
+        size, where = out[0].numel, out[0].device.index
     else:
         out = api._rank_tensors(out, "allreduce_mx4 out")
         size, where = out[0].numel(), out[0].get_device()

@@ -198,6 +198,25 @@ def test_adamw8_refusals(change, status, text):
     refused(ddp.adamw8_step_multi, adamw_args(**change), status, text)
 
 
+@pytest.mark.parametrize("order", ["lists", "interleaved", "shuffled"])
+@pytest.mark.parametrize("pair", [("w", "m"), ("m", "scales"), ("g", "v"), ("w", "w")])
+def test_adamw8_overlaps_among_many(order, pair):
+    """40 tensors of five lists that lie in order, turn by turn or anywhere:
+    one buffer moved a byte (or an element) into another is refused."""
+    T, size = 40, {"g": 200, "w": 400, "m": 100, "v": 100, "scales": 8}
+    names = list(size)
+    slots = [(k, t) for k in names for t in range(T)] if order == "lists" else [(k, t) for t in range(T) for k in names]
+    if order == "shuffled":
+        import random
+        random.Random(1).shuffle(slots)
+    place = {slot: BASE + 1024 * i for i, slot in enumerate(slots)}
+    one, other = (pair[0], 7), (pair[1], 23)
+    place[other] = place[one] + size[pair[0]] - (4 if pair[1] == "w" else 2 if pair[1] in ("g", "scales") else 1)
+    lists = {k: [place[k, t] for t in range(T)] for k in names}
+    refused(ddp.adamw8_step_multi, adamw_args(numels=[100] * T, grads=lists["g"], w=lists["w"], m=lists["m"], v=lists["v"],
+                                              scales=lists["scales"], params=None, norm=None), N.DDP_E_OVERLAP)
+
+
 def test_adamw8_null_lists():
     assert N.lib().adamw8_step_multi(1, (ctypes.c_int64 * 1)(5), N.pointer_array([at(0)]), 0, N.pointer_array([at(1)]),
                                      N.pointer_array([at(2)]), N.pointer_array([at(3)]), None, None, 0, 1e-3, 0.9, 0.9,
@@ -248,9 +267,6 @@ class Gpu(torch.Tensor):
     """A CPU tensor that says it lives on the GPU."""
     is_cuda = True
 
-    def __getitem__(self, k):
-        return torch.Tensor._make_subclass(Gpu, torch.Tensor.__getitem__(self.as_subclass(torch.Tensor), k))
-
 
 def gpu(n, dtype=torch.uint8):
     return torch.Tensor._make_subclass(Gpu, torch.zeros(n, dtype=dtype))
@@ -287,7 +303,8 @@ def test_moments8_sizes():
         ddp.Moments8.zeros([])
 
 
-def test_tensor_level_refusals():
+def test_tensor_level_refusals(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)      # a CPU tensor's
     row = ddp.Mx4(gpu(64), gpu(4), 100)
     with pytest.raises(TypeError):
         ddp.mx4_dequantize([gpu(64)])
@@ -297,9 +314,8 @@ def test_tensor_level_refusals():
         ddp.mx4_dequantize([row, ddp.Mx4(gpu(16), gpu(1), 20)])
     with pytest.raises(ValueError):
         ddp.allreduce_mx4([row] * 17)
-    row.codes.resize_(48)
     with pytest.raises(ValueError):
-        ddp.mx4_dequantize([row])
+        ddp.mx4_quantize([gpu(100, torch.float32)], out=[row, row])
     mom = ddp.Moments8([gpu(100)], [gpu(100)], [gpu(8)])
     mg = ddp.MultiGrad(gpu(100, torch.float32))
     w = gpu(100, torch.float32)
@@ -310,6 +326,39 @@ def test_tensor_level_refusals():
     run = mg.bind_adamw8(w, mom)
     with pytest.raises(ValueError):
         run(1e-3, 1, max_norm=1.0)
-    mom.scales[0].data = torch.zeros(8, dtype=torch.uint8)
+    w.data = torch.zeros(100)
     with pytest.raises(ValueError, match="bind it again"):
         run(1e-3, 1)
+
+
+def test_resized_storages_are_refused():
+    codes, scales = gpu(64), gpu(4)
+    row = ddp.Mx4(codes, scales, 100)
+    part = row.narrow(32, 32)
+    scales.untyped_storage().resize_(0)
+    for r in (row, part):
+        with pytest.raises(ValueError, match="resized"):
+            ddp.mx4_dequantize([r])
+    m = gpu(100)
+    mom = ddp.Moments8([m], [gpu(100)], [gpu(8)])
+    run = ddp.MultiGrad(gpu(100, torch.float32)).bind_adamw8(gpu(100, torch.float32), mom)
+    m.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="resized"):
+        run(1e-3, 1)
+
+
+def test_objects_keep_the_memory_they_were_made_of():
+    """A tensor that is given other memory, or another size in the same, is no
+    longer a part of the object; the object's own views are."""
+    codes, m = gpu(64), gpu(100)
+    row, mom = ddp.Mx4(codes, gpu(4), 100), ddp.Moments8([m], [gpu(100)], [gpu(8)])
+    at, mom_at = row.codes_at, list(mom._held[0].at)
+    assert at == codes.data_ptr() == row.codes.data_ptr() and mom_at == [m.data_ptr()] == [mom.m[0].data_ptr()]
+    codes.data = torch.zeros(64, dtype=torch.uint8)
+    m.resize_(50)
+    mom.m[0].data = torch.zeros(100, dtype=torch.uint8)
+    assert row.codes_at == at == row.codes.data_ptr() and row.codes.numel() == 64
+    assert mom.m[0].data_ptr() == mom_at[0] and mom.m[0].numel() == 100
+    rows = ddp.Mx4.rows(3, 1000, "cpu")
+    assert all(r.codes.numel() == 512 and r.scales.numel() == 32 and r.codes_at % 16 == rows[0].codes_at % 16 for r in rows)
+    assert len({r.codes_at for r in rows} | {r.scales_at for r in rows}) == 6
