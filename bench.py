@@ -767,6 +767,85 @@ def _w_train_step(ctx):
                 run, plan.total * (8 * 2 + 4 + 4 + 24 + 2), None, 3)
 
 
+@work("mx4-quantize-resnet50", "resnet")
+def _w_mx4_quantize(ctx):
+    import torch
+
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, rows = _resnet(ctx)
+    coded = [plan.alloc_mx4(8) for _ in range(2)]
+    left = [[x[:plan.total] for x in plan.alloc_arena(8, torch.bfloat16).zero_()] for _ in range(2)]
+    return Work("resnet50 p8 f32 gradients to 4 bits with bf16 residuals, every rank's flat buffer",
+                lambda i: ddp.mx4_quantize(rows[i % 2][0], residual=left[i % 2], out=coded[i % 2]),
+                8 * plan.total * (4 + 2 + 2 + 17 / 32), "mx4_quantize_kernel<false, 2>", 1)
+
+
+def _vit_mx4(ctx):
+    """The ViT rank gradients in 4 bits, with their residuals, two buffer sets."""
+    import torch
+
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, rows, _, _ = _vit(ctx)
+    coded = [plan.alloc_mx4(8) for _ in range(2)]
+    left = [[x[:plan.total] for x in plan.alloc_arena(8, torch.bfloat16).zero_()] for _ in range(2)]
+    for k in range(2):
+        ddp.mx4_quantize(rows[k][0], residual=left[k], out=coded[k])
+    return plan, rows, coded, left
+
+
+@work("mx4-allreduce-vitb16-one-copy", "vit")
+def _w_mx4_reduce(ctx):
+    import torch
+
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, _, coded, _ = _vit_mx4(ctx)
+    outs = [torch.empty(plan.total, device=_dev()) for _ in range(2)]
+    return Work("vitb16 p8 4-bit gradients: mean into one float32 copy with its norm",
+                lambda i: ddp.allreduce_mx4_norm(coded[i % 2], "mean", out=[outs[i % 2]]),
+                plan.total * (8 * 17 / 32 + 4), "mx4_reduce_kernel<8, 0>", 2)
+
+
+def _vit_adamw8(ctx):
+    """The ViT set's AdamW step with 8-bit moments on one replica's flat buffer:
+    float32 gradient, clipped by a norm, with a bf16 copy of the weights."""
+    import torch
+
+    import gradient_all_reduce_allreduce_amd as ddp
+    import workloads
+    plan = _vit(ctx)[0]
+    w = workloads.torch_normal_(plan.alloc_state(1)[0], 0.02, seed=7)
+    grad = workloads.torch_normal_(torch.empty(plan.total, device=_dev()), 1e-3, seed=8)
+    params = torch.empty(plan.total, dtype=torch.bfloat16, device=_dev())
+    return grad, ddp.MultiGrad(grad).bind_adamw8(w, ddp.Moments8.zeros(grad), params)
+
+
+@work("adamw8-vitb16", "vit")
+def _w_adamw8(ctx):
+    import torch
+    plan = _vit(ctx)[0]
+    _, step = _vit_adamw8(ctx)
+    norm = torch.full((), 9.3, device=_dev())
+    return Work("vitb16 f32 gradient (flat), clipped AdamW step on fp32 w and 8-bit moments with a bf16 copy",
+                lambda i: step(1e-3, i + 1, norm=norm, max_norm=1.0), plan.total * (4 + 8 + 4 + 1 / 8 + 2),
+                "adamw8_kernel<false, 2>", 1)
+
+
+@work("train-step-mx4-vitb16", "vit")
+def _w_train_step_mx4(ctx):
+    import gradient_all_reduce_allreduce_amd as ddp
+    plan, rows, coded, left = _vit_mx4(ctx)
+    grad, step = _vit_adamw8(ctx)
+
+    def run(i):
+        ddp.mx4_quantize(rows[i % 2][0], residual=left[i % 2], out=coded[i % 2])
+        _, norm = ddp.allreduce_mx4_norm(coded[i % 2], "mean", out=[grad])
+        step(1e-3, i + 1, norm=norm, max_norm=1.0)
+    return Work("vitb16 p8 bf16: to 4 bits with bf16 residuals, mean into one float32 copy with its norm, AdamW with "
+                "8-bit moments clipped by it, bf16 weights out",
+                run, plan.total * (8 * (2 + 2 + 2 + 17 / 32) + 8 * 17 / 32 + 4 + 4 + 8 + 4 + 1 / 8 + 2), None, 4,
+                note="what one GPU of eight does is an eighth of the coding and of the sum, and the step")
+
+
 @work("packed-step-ragged2000", "ragged")
 def _w_ragged_step(ctx):
     import gradient_all_reduce_allreduce_amd as ddp

@@ -35,6 +35,7 @@ Tensor-level helpers:
 
 import ctypes
 import functools
+import operator
 
 import numpy as np
 
@@ -1114,7 +1115,8 @@ class MultiGrad:
         return w, m, v, scales, params
 
     def _adamw(self, bound, lr, step, betas, eps, weight_decay, norm, max_norm, seed=None):
-        """``seed``: of a step with 8-bit moments, else None."""
+        """``bound``: w, m, v and params, or with 8-bit moments w, m, v, scales
+        and params, which also take the ``seed``."""
         import torch
         if (norm is None) != (max_norm is None):
             raise ValueError("adamw: norm and max_norm come together")
@@ -1132,10 +1134,10 @@ class MultiGrad:
         args = [count, numels, ptrs, torch_dtype_code(self.grads[0].dtype), *(x.ptrs for x in state), pptrs, pcode, lr,
                 betas[0], betas[1], eps, weight_decay, step, step_dev]
         end = (norm_dev, max_norm or 0.0, _raw_stream(self._index))
-        if seed is None:
+        if len(state) == 3:
             _check(N.lib().adamw_step_multi(*args, *end))
         else:
-            _check(N.lib().adamw8_step_multi(*args, seed, *end))
+            _check(N.lib().adamw8_step_multi(*args, operator.index(seed), *end))
 
 
 def _present(grads, out=None):

@@ -194,7 +194,7 @@ def _allreduce(coded, op, out, out_dtype, residual, with_norm):
         with torch.cuda.device(index):
             return _allreduce(coded, op, out, out_dtype, residual, with_norm)
     out = list(out) if out is not None else _new_rows(P, n, out_dtype or torch.float32, device)
-    again = bool(out) and isinstance(out[0], Mx4)
+    again = any(isinstance(o, Mx4) for o in out)
     if again:
         out, out_codes, out_scales = _coded_rows(out, "allreduce_mx4 out")
         size, where = out[0].numel, out[0].device.index

@@ -651,3 +651,105 @@ def test_two_jobs_on_two_streams():
     torch.cuda.synchronize()
     for (x, _), want in zip(jobs, wanted):
         assert all(torch.equal(p, q) for p, q in zip(job_state(x), want))
+
+
+def test_two_graphs_replayed_in_turn():
+    """Two captured jobs share neither workspace nor scratch memory: replayed in
+    turn and on two streams, each goes on as its eager twin does."""
+    n = 1_000_003
+    twins = [job(n, 3, seed) for seed in (0, 40)]
+    jobs = [job(n, 3, seed) for seed in (0, 40)]
+    for _, once in twins + jobs:
+        once()
+    graphs = []
+    for _, once in jobs:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                once()
+        torch.cuda.current_stream().wait_stream(side)
+        graphs.append((graph, side))
+    for k in range(3):
+        for (graph, side), (_, eager) in zip(graphs, twins):
+            if k == 1:
+                graph.replay()
+            else:
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    graph.replay()
+            eager()
+        torch.cuda.synchronize()
+        for (a, _), (b, _) in zip(twins, jobs):
+            for i, (p, q) in enumerate(zip(job_state(a), job_state(b))):
+                assert torch.equal(p, q), (k, i)
+
+
+def test_with_another_gpu_current(monkeypatch):
+    """A call that finds another GPU current makes the tensors' one current for
+    its launches (seen from one GPU: the first question is answered wrongly, the
+    results are the same)."""
+    n = 5000
+    a, once = job(n, 2, 0)
+    once()
+    x, _ = job(n, 2, 0)
+    real, wrong = torch.cuda.current_device, []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: wrong.pop() if wrong else real())
+    step = ddp.MultiGrad(x["grad"]).bind_adamw8(x["w"], x["moments"])
+    read = x["moments"].bind_read(*x["read"])
+    x["count"] += 1
+    calls = [lambda: ddp.mx4_quantize(x["rows"], residual=x["left"], out=x["coded"]),
+             lambda: ddp.allreduce_mx4(x["coded"], "mean", out=[x["again"]], residual=x["owner"]),
+             lambda: x.update(norm=ddp.allreduce_mx4_norm(x["coded"], "mean", out=[x["grad"]])[1]),
+             lambda: step(1e-3, x["count"], norm=x["norm"], max_norm=1.0, seed=4), read,
+             lambda: x.update(values=ddp.mx4_dequantize(x["coded"]))]
+    for call in calls:
+        wrong.append(real() + 1)
+        call()
+        assert not wrong
+    monkeypatch.undo()
+    assert all(torch.equal(p, q) for p, q in zip(job_state(a), job_state(x)))
+    assert torch.equal(x["values"][1], ddp.mx4_dequantize(a["coded"])[1])
+
+
+def test_moments_read_back_go_on_in_32_bits():
+    """The 8-bit step's weights are those of the 32-bit step on the moments read
+    back before it."""
+    numels = [3000, 41]
+    host, _, x = adamw_case(numels, "f32", None, False)
+    mom = ddp.Moments8(x["m"], x["v"], x["s"])
+    m, v = mom.read()
+    w = [t.clone() for t in x["w"]]
+    ddp.adamw_step(x["g"], w, m, v, 1e-2, 7, (0.9, 0.99), 1e-8, 0.1)
+    ddp.adamw8_step(x["g"], x["w"], mom, 1e-2, 7, (0.9, 0.99), 1e-8, 0.1, seed=1)
+    for i in range(2):
+        bound = mx.weight_bound(host["g"][i], host["w"][i], host["m"][i], host["v"][i], host["s"][i], f(1),
+                                *HYPER.values(), 7)
+        assert_weights(host_of(x["w"][i]), host_of(w[i]), bound, f"w[{i}]")
+        # the codes lie next to the 32-bit moments: within one step of a code, 1/8 of
+        # the value or of the least code's distance
+        for got, want, least in ((mom.read()[0][i], m[i], 2.0 ** -9), (mom.read()[1][i], v[i], 2.0 ** -31)):
+            scale = np.repeat(host_of(mom.scales[i]).reshape(-1, 2)[:, 0 if want is m[i] else 1].astype(float), 32)
+            scale = 2.0 ** (scale[:numels[i]] - 127)
+            d = np.abs(host_of(got).astype(np.float64) - host_of(want))
+            assert (d <= np.maximum(np.abs(host_of(want)) / 8 * (1 + 2.0 ** -20), least * scale * 1.0001)).all()
+
+
+def test_same_call_same_bits():
+    n = 300_007
+    a, first = job(n, 4, 0)
+    b, second = job(n, 4, 0)
+    for _ in range(3):
+        first(), second()
+    assert all(torch.equal(p, q) for p, q in zip(job_state(a), job_state(b)))
+    # another seed rounds otherwise
+    g = torch.ones(n, device=DEV)
+    states = [ddp.Moments8.zeros(g) for _ in range(2)]
+    for seed, mom in enumerate(states):
+        ddp.adamw8_step(g * 0.3, torch.zeros(n, device=DEV), mom, 1e-3, 1, (0.9, 0.99), seed=seed)
+    share = (states[0].m[0] != states[1].m[0]).float().mean()
+    # m = 0.03 lies between 0.0293 (15 * 2^-9) and 0.03125: up with p = 0.36, so two seeds differ at
+    # 2 p (1 - p) = 0.46 of the elements; deviation 0.5 / sqrt(n) = 0.0009, five of those
+    p = float((f(0.1) * f(0.3)) * 512 - 15)
+    assert abs(float(share) - 2 * p * (1 - p)) < 0.0046

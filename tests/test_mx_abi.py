@@ -362,3 +362,88 @@ def test_objects_keep_the_memory_they_were_made_of():
     rows = ddp.Mx4.rows(3, 1000, "cpu")
     assert all(r.codes.numel() == 512 and r.scales.numel() == 32 and r.codes_at % 16 == rows[0].codes_at % 16 for r in rows)
     assert len({r.codes_at for r in rows} | {r.scales_at for r in rows}) == 6
+
+
+# ---------------------------------------------- what the calls hold ----
+
+class Lib:
+    """The library with its launching calls written down instead of made."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name in ("adamw_step_multi", "adamw8_step_multi", "adamw8_read_multi", "mx4_quantize", "mx4_dequantize",
+                    "allreduce_mx4", "allreduce_mx4_coded"):
+            return lambda *args: self.calls.append((name, args)) or N.DDP_OK
+        return getattr(self.real, name)
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    from gradient_all_reduce_allreduce_amd import api
+    stub = Lib(N.lib())
+    monkeypatch.setattr(N, "lib", lambda: stub)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)    # a CPU tensor's device index
+    monkeypatch.setattr(api, "_raw_stream", lambda index: 0)
+    return stub
+
+
+def step8(g, params=None):
+    f32 = [gpu(x.numel(), torch.float32) for x in g]
+    mom = ddp.Moments8([gpu(x.numel()) for x in g], [gpu(x.numel()) for x in g], [gpu(2 * -(-x.numel() // 32)) for x in g])
+    return f32, mom
+
+
+def test_eight_bit_state_never_goes_to_the_32_bit_step(lib):
+    """Whatever is given for the seed: 8-bit moments reach their own call, or
+    the call is refused."""
+    g = [gpu(100, torch.float32), gpu(7, torch.float32)]
+    w, mom = step8(g)
+    run = ddp.MultiGrad(g).bind_adamw8(w, mom)
+    run(1e-3, 1)
+    run(1e-3, 1, seed=-5)
+    run(1e-3, 1, seed=True)
+    for bad in (None, 1.5, "1"):
+        with pytest.raises(TypeError):
+            run(1e-3, 1, seed=bad)
+    assert [name for name, _ in lib.calls] == ["adamw8_step_multi"] * 3
+    assert [args[17] for _, args in lib.calls] == [0, -5, 1]
+    args = lib.calls[0][1]
+    assert list(args[5]) == [x.data_ptr() for x in mom.m] and list(args[7]) == [x.data_ptr() for x in mom.scales]
+
+
+def test_nothing_outlives_a_step(lib):
+    import gc
+    import weakref
+    gc.disable()
+    try:
+        for bound in (False, True):
+            g = [gpu(100, torch.float32)]
+            w, mom = step8(g)
+            refs = [weakref.ref(x) for x in (*g, *w, mom)]
+            if bound:
+                run = ddp.MultiGrad(g).bind_adamw8(w, mom)
+                run(1e-3, 1)
+                read = mom.bind_read(gpu(100, torch.float32), gpu(100, torch.float32))
+                read()
+                del run, read
+            else:
+                ddp.adamw8_step(g, w, mom, 1e-3, 1)
+            del g, w, mom
+            assert all(r() is None for r in refs), bound
+    finally:
+        gc.enable()
+
+
+def test_a_bound_step_keeps_its_memory(lib):
+    import weakref
+    g = [gpu(100, torch.float32)]
+    w, mom = step8(g)
+    storages = [x.data_ptr() for x in (mom.m[0], w[0])]
+    run = ddp.MultiGrad(g).bind_adamw8(w, mom)
+    held = weakref.ref(g[0])
+    del g, w, mom
+    assert held() is not None
+    run(1e-3, 2)
+    assert [lib.calls[-1][1][5][0], lib.calls[-1][1][4][0]] == storages
