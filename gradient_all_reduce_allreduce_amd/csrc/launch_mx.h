@@ -25,11 +25,13 @@ constexpr int mx4_dequantize_wg_per_cu(bool bf16) { return bf16 ? 5 : 4; }
 // The all-reduce (figures in mx4_reduce.hip).  Spans per wave: two where a span
 // moves little, few ranks and no float32.
 constexpr int mx4_reduce_spans(int P, bool f32) { return !f32 && P <= 4 ? 2 : 1; }
-// Workgroups per CU where every rank receives values, 0 for no limit.
-constexpr int mx4_reduce_wg_per_cu(int P, bool f32, bool all_ranks, bool coded) {
-    if (!all_ranks || coded || P == 1) return 0;
-    if (f32) return P <= 3 ? 4 : P <= 6 ? 2 : 1;
-    return P <= 6 ? 4 : P <= 8 ? 3 : P <= 12 ? 2 : 1;
+// Workgroups per CU, 0 for no limit: fewer the more every rank receives as
+// values; one more of those with float32 and the norm, whose sums they wait for.
+constexpr int mx4_reduce_wg_per_cu(int P, bool f32, bool all_ranks_values, bool norm) {
+    if (!all_ranks_values) return 0;
+    if (!f32) return P <= 6 ? 5 : P <= 12 ? 3 : 1;
+    if (P > 6) return 1;
+    return (P <= 2 ? 5 : P <= 3 ? 4 : 2) + (norm ? 1 : 0);
 }
 
 // The AdamW step with 8-bit moments and their reading back (adamw8.hip).

@@ -8,6 +8,32 @@
 // mx4.hip does, with a left-over of the owner's) for the way back.  The codes
 // of a block travel once and whole, to an owner that adds the P copies, so the
 // order is the same for every element, whatever the chunks.
+//
+// Bound by HBM: 17/32 byte an element and rank in, 4 or 2 (or 17/32) out for
+// each copy, against 1.6 instructions an element and rank.  86.6M elements: 8 ranks
+// into one float32 copy 111 us, 6.4 TB/s; with the norm 116, its partials' sum
+// 4 of them; 16 ranks coded again with a float32 left-over 233 us, 6.3 TB/s.
+//
+// Layout (mx.h): codes as they lie, 8 elements a lane, so that a wave decodes 512
+// elements with one dword and one byte a rank in each lane, all ranks' loads in
+// flight at once; float32 results go through LDS to whole lines (without that,
+// 16 bytes of every 32 by an instruction, 125 us; loading codes in the order of
+// whole float32 lines instead, which halves what a load's lanes share of a line,
+// 157).  Two spans a wave, not one, where a span is little to load: 4 ranks
+// coded again 128 us against 138 with every rank written, 47 against 41 with one
+// copy.  Workgroups of 4 waves keep the 128 bytes of scales that 4,096 elements
+// have in one or two L2s; one-wave workgroups took 146 us for the first case.
+//
+// One copy runs fastest with the CUs full.  Every rank written as values is
+// nearly all writes, many streams at once, and wants fewer: us for 86.6M elements by
+// workgroups per CU 0 (full), 1, 2, 3, 4, 5, 6 --
+//     float32  P = 2   151  230  164  149  131  125  147
+//              P = 4   314  331  273  274  304  306  308
+//              P = 8   643  537  602  621  624  632  644
+//     bf16     P = 2    74  130   99   81   73   72   74
+//              P = 8   326  403  328  306  311  331  331
+//     with norm, float32  P = 2  154  285  217  174  155  138  132
+//                         P = 4  318  336  357  274  297  310  312
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -222,7 +248,7 @@ int launch_mx4_reduce(const Mx4Reduce& l, int64_t* workgroups, const char** msg)
     *workgroups = grid;
     void* args[] = {&a};
     const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kMxLanes), args,
-                                         lds_for(mx4_reduce_wg_per_cu(l.P, f32, l.n_out > 1, coded), f32),
+                                         lds_for(mx4_reduce_wg_per_cu(l.P, f32, l.n_out > 1 && !coded, l.partials != nullptr), f32),
                                          static_cast<hipStream_t>(l.stream));
     if (e == hipSuccess) return 0;
     *msg = "hipLaunchKernel(mx4_reduce)";
