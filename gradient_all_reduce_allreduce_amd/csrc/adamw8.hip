@@ -18,14 +18,29 @@
 // to nearest, a moment stops where its change per step falls under half a step
 // of its code: v, which moves by (1 - b2) of itself, at a sixteenth of its
 // value for b2 = 0.999, and the weights' steps come out several times too long.
-// At random, the expected moment is the exact one.  With one step's share of
-// (1 - b2) and codes d apart (d = 1/16 .. 1/8 of the value) a stationary v has
-// a relative standard deviation of about sqrt(d / 2), 20-25%, from the rounding,
-// whatever b2; m, which moves by more than its code's step, about 8%.
+// At random, the expected moment is the exact one.  Codes are d = 1/16 to 1/8 of
+// the value apart, and a v whose steps are smaller than that varies about the
+// exact one by sqrt(d / 2) of it, whatever b2 (18% with normal gradients and b2 =
+// 0.99, 20% with 0.999, no offset); m, whose steps are larger, by 9% of its own
+// root mean square.
 //
 // A block of m with an infinity or a NaN has s = 255 and is NaN as a whole from
 // the next step on, one of v infinite.  A norm that is not finite leaves
 // everything as it was.
+//
+// Bound by HBM: 16.1 bytes an element with bf16 gradient and copy (32-bit moments:
+// 28) against 42 instructions.  86.6M elements, bf16 gradient and copy: 221 us, 6.3
+// TB/s, with the count on the GPU 222; float32 gradient without copy 221, one
+// element off a line 236.  Read back as bf16 82 us, 6.4 TB/s, as float32 130, 6.7.
+//
+// Layout: a workgroup of 4 waves takes a tile of 2,048 elements, a wave two spans
+// of 256, all loads of both first; a lane has 4 consecutive elements, 16 bytes of
+// the weights, and 8 lanes a block.  Blocks count from the tensor's first element,
+// so tiles do too, wherever that lies in a line.  One span a wave: 223 us, but 252
+// with the count on the GPU, whose powers every wave works out; four 226.  By
+// workgroups per CU 0 (full), 2, 3, 4, 5, 6, 8: 228 261 227 221 227 224 226 us.
+// Addresses and sizes travel in the kernel arguments, as in adamw.hip, 162 tensors
+// a launch (139 with copies of the weights).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -49,27 +64,28 @@ constexpr int kSpans = 2;
 constexpr uint32_t kTileElems = 4 * kSpans * kSpan;
 constexpr uint32_t kBlockElems = DDP_MX_BLOCK;
 constexpr uint32_t kMaxGrid = 1u << 23;
-// Tensors (or pieces of them) per launch: as many as the arguments hold.
-constexpr int kCap = 120;
-
+// Consecutive tensors of a call, as many as the arguments hold (PARAMS: with
+// their copies), empty ones among them; or one piece of a tensor that is longer
+// than kMaxPiece.
+template <bool PARAMS>
 struct Adam8Args {
+    static constexpr int kCap = PARAMS ? 139 : 162;
     const char* g[kCap];
     char* w[kCap];
     char* m[kCap];
     char* v[kCap];
     char* s[kCap];
-    char* p[kCap];
-    uint32_t count[kCap];      // elements, up to kMaxPiece
+    char* p[PARAMS ? kCap : 1];
+    uint32_t count[kCap];      // elements
     uint32_t first_tile[kCap];
-    uint32_t tensor[kCap];     // which tensor of the call a piece belongs to,
-    uint32_t piece[kCap];      // and which of its pieces it is
     int32_t n;
     uint32_t tiles;
+    uint32_t tensor;           // the first one's number in the call
+    uint32_t piece;            // and which of its pieces it is
     uint32_t seed;             // the seed's two halves mixed
     adamw::Scalars scalars;
 };
-static_assert(sizeof(Adam8Args) <= kArgBytes, "kernel arguments");
-typedef const __attribute__((address_space(4))) Adam8Args* KAdam8;
+static_assert(sizeof(Adam8Args<false>) <= kArgBytes && sizeof(Adam8Args<true>) <= kArgBytes, "kernel arguments");
 
 // Random bits.  32 per element, from a key and the element's place in its
 // piece: a multiplication by 2^32 over the golden ratio steps through all
@@ -136,10 +152,11 @@ __device__ __forceinline__ uint32_t top_bytes(const uint32_t (&x)[4]) {
 }
 
 // The weights' step, the root and the quotient by the hardware's instructions,
-// within 1 ulp each (correctly rounded ones take 40 instructions an element, and
-// this kernel would be bound by them: 230 us for 86.6M elements instead of 212):
-// beside moments of 3 bits that says nothing.  A second moment below 2^-126,
-// which those instructions take for zero, counts as that.
+// within 1 ulp each: beside moments of 3 bits of mantissa a correctly rounded one
+// says nothing more.  (With those, and codes made by conversions, comparisons and
+// selections, the step took 93 instructions an element and was bound by them, 229
+// us.)  A second moment below 2^-126, which these instructions take for zero,
+// counts as that.
 __device__ __forceinline__ float step_weight(float w, float m, float v, const adamw::Factors& f) {
 #pragma clang fp contract(off)
     const float least = __uint_as_float(mx::larger(__float_as_uint(v), 1u << 23));
@@ -174,7 +191,7 @@ __device__ __forceinline__ void store_bytes(char* p, int64_t i, int64_t n, uint3
         if (i + e < n) p[i + e] = static_cast<char>(x >> (8 * e));
 }
 
-// The last piece that starts at or before the tile.
+// The last tensor that starts at or before the tile.
 template <class A>
 __device__ __forceinline__ int piece_of(A a, uint32_t tile) {
     int t = 0;
@@ -279,7 +296,8 @@ __device__ __forceinline__ void step_lane(const Streams& x, int64_t at, const La
 
 // GB: bf16 gradients.  PM: the copy, 0 none, 1 float32, 2 bf16.
 template <bool GB, int PM>
-__global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args) {
+__global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args<PM != 0>) {
+    typedef const __attribute__((address_space(4))) Adam8Args<PM != 0>* KAdam8;
     const KAdam8 a = (KAdam8)(__builtin_amdgcn_kernarg_segment_ptr());
     const uint32_t tiles = a->tiles;
     const adamw::KScalars k = (adamw::KScalars)(&a->scalars);
@@ -288,7 +306,8 @@ __global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int t = piece_of(a, tile);
-        const Streams x = {a->g[t], a->w[t], a->m[t], a->v[t], a->s[t], a->p[t], a->count[t]};
+        const Streams x = {a->g[t], a->w[t], a->m[t], a->v[t], a->s[t], PM != 0 ? a->p[PM != 0 ? t : 0] : nullptr,
+                           a->count[t]};
         const int64_t at = (static_cast<int64_t>(tile - a->first_tile[t]) * 4 + wave) * (kSpans * kSpan);
         const bool whole = at + kSpans * kSpan <= x.n;
         Lane l[kSpans];
@@ -302,7 +321,7 @@ __global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args) {
         if (!adamw::factors(k, norm, step, f)) return;
         uint32_t key = mix_word(a->seed, static_cast<uint32_t>(step));
         key = mix_word(key, static_cast<uint32_t>(step >> 32));
-        key = mix_word(mix_word(key, a->tensor[t]), a->piece[t]);
+        key = mix_word(mix_word(key, a->tensor + t), a->piece);
         if (whole) {
 #pragma unroll
             for (int u = 0; u < kSpans; ++u) step_lane<GB, PM, true>(x, at + u * kSpan, l[u], f, key);
@@ -328,6 +347,7 @@ const void* kernel_for(const AdamWLaunch& l) {
 // The moments' values.
 constexpr int read_spans(bool bf16) { return bf16 ? 2 : 1; }
 struct Read8Args {
+    static constexpr int kCap = 164;
     const char* m[kCap];
     const char* v[kCap];
     const char* s[kCap];
@@ -409,44 +429,61 @@ int launch(const void* fn, void* args, uint32_t tiles, unsigned lds, void* strea
     return static_cast<int>(e);
 }
 
-}  // namespace
+// A launch's tensors, from tensor t on: fill(slot, tensor, first element)
+// for each, until the arguments are full or a tensor is too long for one launch,
+// whose pieces (`at`: the next one's first element) go alone.
+template <class A, class F>
+void fill_launch(A& a, int32_t n_tensors, const int64_t* numels, int64_t tile, int32_t& t, int64_t& at, F fill) {
+    int64_t tiles = 0;
+    for (a.n = 0; t < n_tensors && a.n < A::kCap;) {
+        const bool alone = numels[t] > kMaxPiece;
+        if (alone && a.n > 0) break;
+        const int64_t count = std::min(numels[t] - at, kMaxPiece);
+        fill(a.n, t, at);
+        a.count[a.n] = static_cast<uint32_t>(count);
+        a.first_tile[a.n] = static_cast<uint32_t>(tiles);
+        tiles += (count + tile - 1) / tile;
+        ++a.n;
+        at += count;
+        if (at >= numels[t]) {
+            ++t;
+            at = 0;
+        }
+        if (alone) break;
+    }
+    a.tiles = static_cast<uint32_t>(tiles);
+}
 
-int launch_adamw8(const AdamW8Launch& l, const char** msg) {
+template <bool PARAMS>
+int launch_step(const AdamW8Launch& l, const char** msg) {
     const AdamWLaunch& b = l.step;
-    Adam8Args a;
+    Adam8Args<PARAMS> a;
     a.scalars = adamw::scalars_of(b);
     a.seed = mix_word(mix_word(0, static_cast<uint32_t>(l.seed)), static_cast<uint32_t>(l.seed >> 32));
     const void* fn = kernel_for(b);
-    int64_t at = 0;   // element of tensor t that the next piece starts at
+    int64_t at = 0;
     for (int32_t t = 0; t < b.n_tensors;) {
-        int64_t tiles = 0;
-        for (a.n = 0; t < b.n_tensors && a.n < kCap;) {
-            const int64_t count = std::min(b.numels[t] - at, kMaxPiece);
-            if (count > 0) {
-                a.g[a.n] = static_cast<const char*>(b.grads[t]) + at * (b.grad_bf16 ? 2 : 4);
-                a.w[a.n] = reinterpret_cast<char*>(b.w[t] + at);
-                a.m[a.n] = reinterpret_cast<char*>(l.m[t] + at);
-                a.v[a.n] = reinterpret_cast<char*>(l.v[t] + at);
-                a.s[a.n] = reinterpret_cast<char*>(l.scales[t] + at / kBlockElems * 2);
-                a.p[a.n] = b.params != nullptr ? static_cast<char*>(b.params[t]) + at * (b.param_bf16 ? 2 : 4) : nullptr;
-                a.count[a.n] = static_cast<uint32_t>(count);
-                a.first_tile[a.n] = static_cast<uint32_t>(tiles);
-                a.tensor[a.n] = static_cast<uint32_t>(t);
-                a.piece[a.n] = static_cast<uint32_t>(at / kMaxPiece);
-                tiles += (count + kTileElems - 1) / kTileElems;
-                at += count;
-                ++a.n;
-            }
-            if (at >= b.numels[t]) {
-                ++t;
-                at = 0;
-            }
-        }
-        if (a.n == 0) continue;
-        a.tiles = static_cast<uint32_t>(tiles);
-        if (const int e = launch(fn, &a, a.tiles, lds_reserve(kAdamW8WgPerCu), b.stream, "hipLaunchKernel(adamw8)", msg)) return e;
+        a.tensor = static_cast<uint32_t>(t);
+        a.piece = static_cast<uint32_t>(at / kMaxPiece);
+        fill_launch(a, b.n_tensors, b.numels, kTileElems, t, at, [&](int k, int32_t i, int64_t from) {
+            a.g[k] = static_cast<const char*>(b.grads[i]) + from * (b.grad_bf16 ? 2 : 4);
+            a.w[k] = reinterpret_cast<char*>(b.w[i] + from);
+            a.m[k] = reinterpret_cast<char*>(l.m[i] + from);
+            a.v[k] = reinterpret_cast<char*>(l.v[i] + from);
+            a.s[k] = reinterpret_cast<char*>(l.scales[i] + from / kBlockElems * 2);
+            if constexpr (PARAMS) a.p[k] = static_cast<char*>(b.params[i]) + from * (b.param_bf16 ? 2 : 4);
+        });
+        if (a.tiles == 0) continue;
+        if (const int e = launch(fn, &a, a.tiles, lds_reserve(kAdamW8WgPerCu), b.stream, "hipLaunchKernel(adamw8)", msg))
+            return e;
     }
     return 0;
+}
+
+}  // namespace
+
+int launch_adamw8(const AdamW8Launch& l, const char** msg) {
+    return l.step.params != nullptr ? launch_step<true>(l, msg) : launch_step<false>(l, msg);
 }
 
 int launch_adamw8_read(const Moments8Read& l, const char** msg) {
@@ -456,29 +493,18 @@ int launch_adamw8_read(const Moments8Read& l, const char** msg) {
     const int64_t es = l.out_bf16 ? 2 : 4;
     int64_t at = 0;
     for (int32_t t = 0; t < l.n_tensors;) {
-        int64_t tiles = 0;
-        for (a.n = 0; t < l.n_tensors && a.n < kCap;) {
-            const int64_t count = std::min(l.numels[t] - at, kMaxPiece);
-            if (count > 0) {
-                a.m[a.n] = reinterpret_cast<const char*>(l.m[t] + at);
-                a.v[a.n] = reinterpret_cast<const char*>(l.v[t] + at);
-                a.s[a.n] = reinterpret_cast<const char*>(l.scales[t] + at / kBlockElems * 2);
-                a.m_out[a.n] = static_cast<char*>(l.m_out[t]) + at * es;
-                a.v_out[a.n] = static_cast<char*>(l.v_out[t]) + at * es;
-                a.count[a.n] = static_cast<uint32_t>(count);
-                a.first_tile[a.n] = static_cast<uint32_t>(tiles);
-                tiles += mx_tiles(count, read_spans(l.out_bf16));
-                at += count;
-                ++a.n;
-            }
-            if (at >= l.numels[t]) {
-                ++t;
-                at = 0;
-            }
-        }
-        if (a.n == 0) continue;
-        a.tiles = static_cast<uint32_t>(tiles);
-        if (const int e = launch(fn, &a, a.tiles, lds_reserve(kMoments8WgPerCu), l.stream, "hipLaunchKernel(adamw8_read)", msg)) return e;
+        fill_launch(a, l.n_tensors, l.numels, 2048 * read_spans(l.out_bf16), t, at,
+                    [&](int k, int32_t i, int64_t from) {
+                        a.m[k] = reinterpret_cast<const char*>(l.m[i] + from);
+                        a.v[k] = reinterpret_cast<const char*>(l.v[i] + from);
+                        a.s[k] = reinterpret_cast<const char*>(l.scales[i] + from / kBlockElems * 2);
+                        a.m_out[k] = static_cast<char*>(l.m_out[i]) + from * es;
+                        a.v_out[k] = static_cast<char*>(l.v_out[i]) + from * es;
+                    });
+        if (a.tiles == 0) continue;
+        if (const int e = launch(fn, &a, a.tiles, lds_reserve(kMoments8WgPerCu), l.stream, "hipLaunchKernel(adamw8_read)",
+                                 msg))
+            return e;
     }
     return 0;
 }

@@ -68,8 +68,8 @@ constexpr bool has_f32(int out) { return out == kF32 || out == kCodedLeftF32; }
 // s / P, correctly rounded.  For P no power of two by way of the float64
 // quotient, whose rounding to float32 is innocuous, and that from the product
 // with 1 / P and one correction by its remainder, which is exact in a fused
-// multiply-add (Markstein's division; a float64 division took 1.27 times as
-// long for 3 ranks).
+// multiply-add (Markstein's division; with a float64 division 86.6M elements of
+// 3 ranks coded again took 52 us instead of 46).
 template <int P>
 __device__ __forceinline__ float mean_of(float s) {
     if constexpr ((P & (P - 1)) == 0) {

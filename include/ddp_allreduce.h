@@ -1078,8 +1078,11 @@ int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes);
  * bytes an element for both instead of 8.
  *
  * The step is adamw_step_multi's, on decoded moments, and the weights take the
- * new moments before these are rounded.  A block is 32 consecutive elements of
- * a tensor, with two scale bytes, s_m then s_v:
+ * new moments before these are rounded.  The root and the quotient of the
+ * weights' formula are within 1 ulp each, not rounded correctly, with v at least
+ * 2^-126 there; the moments have one rounding per operation as they do in
+ * adamw_step_multi.  A block is 32 consecutive elements of a tensor, with two scale
+ * bytes, s_m then s_v:
  *   m   one byte: sign, 4 bits of exponent, 3 of mantissa (the format E4M3 of
  *       the OCP microscaling specification, up to 448), times 2^(s_m - 127), s_m
  *       the smallest, from 1, that holds the block's maximum
@@ -1095,7 +1098,8 @@ int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes);
  * average.  The 16 random bits of each moment are a hash of seed, step, the
  * tensor's number in the call and the element's in its tensor: the same call
  * gives the same bits, on any stream and in any replay.  Ranks that keep
- * identical replicas need the same seed.
+ * identical replicas need the same seed; calls that share a step's tensors
+ * among them, and so count each from 0, a seed each.
  * A block of m that meets an infinity or NaN becomes NaN as a whole, one of v
  * that passes float32 infinite.
  *

@@ -753,3 +753,43 @@ def test_same_call_same_bits():
     # 2 p (1 - p) = 0.46 of the elements; deviation 0.5 / sqrt(n) = 0.0009, five of those
     p = float((f(0.1) * f(0.3)) * 512 - 15)
     assert abs(float(share) - 2 * p * (1 - p)) < 0.0046
+
+
+@pytest.mark.parametrize("count", [139, 140, 162, 163, 164, 165, 325])
+@pytest.mark.parametrize("params", [None, "bf16"])
+def test_adamw8_at_the_launches_limits(count, params):
+    """As many tensors as a launch holds, and one more; every fifth empty, the
+    last two as well, so that launches end and begin with empty ones."""
+    numels = [0 if t % 5 == 4 or t >= count - 2 else 1 + 53 * t % 300 for t in range(count)]
+    check_adamw8(numels, "f32", params, True)
+    codes = [moments(n, t) for t, n in enumerate(numels)]
+    held = [torch.from_numpy(np.concatenate(x)).to(DEV) for x in zip(*codes)]
+    mom = ddp.Moments8(held[0].split(numels), held[1].split(numels), held[2].split([c[2].size for c in codes]))
+    new = mom.read()
+    for t, c in enumerate(codes):
+        for which, want in enumerate(mx.moments_decode(*c)):
+            assert_same_bits(host_of(new[which][t]), want, f"{which} of {t}")
+
+
+def test_adamw8_long_tensor_among_short_ones():
+    """A tensor of two pieces has launches of its own, and the tensors around it
+    keep their numbers in the call; its values read back past 2^30 too."""
+    numels = [33, 2 ** 30 + 777, 0, 700]
+    g = [torch.zeros(n, dtype=torch.bfloat16, device=DEV) for n in numels]
+    w = [torch.zeros(n, device=DEV) for n in numels]
+    mom = ddp.Moments8.zeros(g)
+    places = {(0, 0): values(33, "bf16", 1), (1, 0): values(640, "bf16", 2), (1, 2 ** 30 - 64): values(64, "bf16", 3),
+              (1, 2 ** 30): values(777, "bf16", 4), (3, 0): values(700, "bf16", 5)}
+    for (t, at), a in places.items():
+        g[t][at:at + a.size] = torch.from_numpy(a).to(DEV)
+    ddp.adamw8_step(g, w, mom, HYPER["lr"], 1, (HYPER["b1"], HYPER["b2"]), HYPER["eps"], HYPER["wd"], seed=8)
+    read = mom.read(torch.bfloat16)
+    for (t, at), a in places.items():
+        zero = np.zeros(a.size, np.uint8)
+        _, mv, vv = oracle.adamw(a, np.zeros(a.size, f), zero.astype(f), zero.astype(f), f(1), *HYPER.values(), 1)
+        m, v, s = mx.moments_encode(mv, vv, mx.random_bits(a.size, 8, 1, t, first=at))
+        got_s = host_of(mom.scales[t][at // 16:at // 16 + s.size])
+        assert np.array_equal(got_s, s) and np.array_equal(host_of(mom.m[t][at:at + a.size]), m), (t, at)
+        assert np.array_equal(host_of(mom.v[t][at:at + a.size]), v), (t, at)
+        for which, want in enumerate(mx.moments_decode(m, v, s)):
+            assert_same_bits(host_of(read[which][t][at:at + a.size]), rounded(want, "bf16"), f"{which} of {t} at {at}")
