@@ -29,7 +29,7 @@
 // everything as it was.
 //
 // Bound by HBM: 16.1 bytes an element with bf16 gradient and copy (32-bit moments:
-// 28) against 42 instructions.  86.6M elements, bf16 gradient and copy: 221 us, 6.3
+// 28) against 64 instructions, 11 of them a wave's own.  86.6M elements, bf16 gradient and copy: 221 us, 6.3
 // TB/s, with the count on the GPU 222; float32 gradient without copy 221, one
 // element off a line 236.  Read back as bf16 82 us, 6.4 TB/s, as float32 130, 6.7.
 //
@@ -154,8 +154,8 @@ __device__ __forceinline__ uint32_t top_bytes(const uint32_t (&x)[4]) {
 // The weights' step, the root and the quotient by the hardware's instructions,
 // within 1 ulp each: beside moments of 3 bits of mantissa a correctly rounded one
 // says nothing more.  (With those, and codes made by conversions, comparisons and
-// selections, the step took 93 instructions an element and was bound by them, 229
-// us.)  A second moment below 2^-126, which these instructions take for zero,
+// selections, an element took 93 instructions instead of 53, and the step was bound
+// by them, 229 us.)  A second moment below 2^-126, which these instructions take for zero,
 // counts as that.
 __device__ __forceinline__ float step_weight(float w, float m, float v, const adamw::Factors& f) {
 #pragma clang fp contract(off)

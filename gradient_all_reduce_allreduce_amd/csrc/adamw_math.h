@@ -43,7 +43,7 @@ typedef const __attribute__((address_space(4))) Scalars* KScalars;
 struct StepFactors {
     float size, root2;
 };
-__host__ __device__ __forceinline__ StepFactors step_factors(double lr, double b1, double b2, int64_t t) {
+inline StepFactors step_factors(double lr, double b1, double b2, int64_t t) {
     double p1 = 1.0, p2 = 1.0;
     for (; t > 0; t >>= 1) {
         if (t & 1) {
@@ -54,6 +54,22 @@ __host__ __device__ __forceinline__ StepFactors step_factors(double lr, double b
         b2 *= b2;
     }
     return {static_cast<float>(lr / (1.0 - p1)), static_cast<float>(1.0 / __builtin_sqrt(1.0 - p2))};
+}
+
+// The same on the GPU, the same for the whole wave: even lanes work out the
+// first of the two, odd lanes the second, with the same operations on each.
+__device__ __forceinline__ StepFactors wave_step_factors(double lr, double b1, double b2, int64_t t) {
+    const bool odd = threadIdx.x & 1;
+    double b = odd ? b2 : b1, p = 1.0;
+    for (; t > 0; t >>= 1) {
+        if (t & 1) p *= b;
+        b *= b;
+    }
+    const double rest = 1.0 - p;
+    const float x = static_cast<float>((odd ? 1.0 : lr) / (odd ? __builtin_sqrt(rest) : rest));
+    const int f = static_cast<int>(__float_as_uint(x));
+    return {__uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(f, 0))),
+            __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(f, 1)))};
 }
 
 inline Scalars scalars_of(const AdamWLaunch& l) {
@@ -120,7 +136,7 @@ __device__ __forceinline__ bool factors(KScalars a, float norm, int64_t t, Facto
     f.root2 = a->root2;
     if (a->step != nullptr) {
         if (t < 1) return false;
-        const StepFactors s = step_factors(a->lr, a->b1, a->b2, t);
+        const StepFactors s = wave_step_factors(a->lr, a->b1, a->b2, t);
         f.step_size = s.size;
         f.root2 = s.root2;
     }
