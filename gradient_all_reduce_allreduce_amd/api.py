@@ -405,21 +405,28 @@ def _ptrs_or_none(ptrs):
     return _ptr_array(ptrs) if ptrs is not None else None
 
 
+def _row_ptrs(ptrs, P):
+    """P addresses or None; a P that the library refuses is left to it."""
+    if ptrs is not None and len(ptrs) < P <= MAX_RANKS:
+        raise ValueError(f"need {P} addresses, got {len(ptrs)}")
+    return _ptrs_or_none(ptrs)
+
+
 def mx4_quantize_rows(P, rank_in, in_dtype, n, rank_residual, residual_dtype, rank_codes, rank_scales, stream=None):
     """``rank_residual``: P addresses or None."""
-    _check(N.lib().mx4_quantize(P, _ptrs_or_none(rank_in), in_dtype, n, _ptrs_or_none(rank_residual), residual_dtype,
-                                _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), stream))
+    _check(N.lib().mx4_quantize(P, _row_ptrs(rank_in, P), in_dtype, n, _row_ptrs(rank_residual, P), residual_dtype,
+                                _row_ptrs(rank_codes, P), _row_ptrs(rank_scales, P), stream))
 
 
 def mx4_dequantize_rows(P, rank_codes, rank_scales, n, rank_out, out_dtype, stream=None):
-    _check(N.lib().mx4_dequantize(P, _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), n,
-                                  _ptrs_or_none(rank_out), out_dtype, stream))
+    _check(N.lib().mx4_dequantize(P, _row_ptrs(rank_codes, P), _row_ptrs(rank_scales, P), n,
+                                  _row_ptrs(rank_out, P), out_dtype, stream))
 
 
 def allreduce_mx4_rows(op, P, rank_codes, rank_scales, n, rank_out, out_dtype, norm=None, workspace=None,
                        workspace_bytes=0, stream=None):
     """``rank_out``: P addresses, or one (a single copy of the result)."""
-    _check(N.lib().allreduce_mx4(_op(op), P, _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), n, len(rank_out),
+    _check(N.lib().allreduce_mx4(_op(op), P, _row_ptrs(rank_codes, P), _row_ptrs(rank_scales, P), n, len(rank_out),
                                  _ptrs_or_none(rank_out), out_dtype, norm, workspace, workspace_bytes, stream))
 
 
@@ -428,7 +435,7 @@ def allreduce_mx4_coded(op, P, rank_codes, rank_scales, n, out_codes, out_scales
     """``out_codes``, ``out_scales``: P addresses each, or one."""
     if len(out_codes) != len(out_scales):
         raise ValueError("out_codes and out_scales must have one entry per row")
-    _check(N.lib().allreduce_mx4_coded(_op(op), P, _ptrs_or_none(rank_codes), _ptrs_or_none(rank_scales), n,
+    _check(N.lib().allreduce_mx4_coded(_op(op), P, _row_ptrs(rank_codes, P), _row_ptrs(rank_scales, P), n,
                                        len(out_codes), _ptrs_or_none(out_codes), _ptrs_or_none(out_scales), residual,
                                        residual_dtype, norm, workspace, workspace_bytes, stream))
 
@@ -1070,17 +1077,18 @@ class MultiGrad:
 
     def _state(self, w, m, v, params):
         """w, m, v and params (or None) as a step takes them."""
+        return self._float_state(w, params, (m, "m"), (v, "v"))
+
+    def _float_state(self, w, params, *moments):
         import torch
         if any(g.dtype != self.grads[0].dtype for g in self.grads):
             raise ValueError("adamw: gradients must all have the same element type")
-        w = self._match(w, "adamw w", (torch.float32,))
-        m = self._match(m, "adamw m", (torch.float32,)) if m is not None else None
-        v = self._match(v, "adamw v", (torch.float32,)) if v is not None else None
+        w, *moments = (self._match(x, f"adamw {what}", (torch.float32,)) for x, what in ((w, "w"), *moments))
         if params is not None:
             params = self._match(params, "adamw params", (torch.float32, torch.bfloat16))
             if any(p.dtype != params.tensors[0].dtype for p in params.tensors):
                 raise ValueError("adamw: params must all have the same element type")
-        return w, m, v, params
+        return (w, *moments, params)
 
     def bind_adamw8(self, w, moments, params=None):
         """``bind_adamw`` with the moments in 8 bits: ``moments`` is a
@@ -1111,7 +1119,7 @@ class MultiGrad:
         if m.numels != self._held.numels or moments.device != self.device:
             raise ValueError("adamw8: need moments of each gradient's size on its device")
         moments._kept.check()
-        w, _, _, params = self._state(w, None, None, params)
+        w, params = self._float_state(w, params)
         return w, m, v, scales, params
 
     def _adamw(self, bound, lr, step, betas, eps, weight_decay, norm, max_norm, seed=None):

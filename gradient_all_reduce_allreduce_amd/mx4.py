@@ -31,6 +31,8 @@ class Mx4:
 
     def __init__(self, codes, scales, numel):
         import torch
+        if numel < 0:
+            raise ValueError(f"Mx4: numel = {numel} is negative")
         for x, what, size in ((codes, "codes", 16 * _blocks(numel)), (scales, "scales", _blocks(numel))):
             if not isinstance(x, torch.Tensor) or x.dtype != torch.uint8:
                 raise TypeError(f"Mx4: {what} must be a uint8 tensor")

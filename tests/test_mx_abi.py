@@ -289,6 +289,19 @@ def test_mx4_sizes():
         ddp.Mx4(gpu(64, torch.int8), gpu(4), 100)
     with pytest.raises(ValueError):
         ddp.Mx4.empty(-1, "cpu")
+    with pytest.raises(ValueError, match="negative"):
+        ddp.Mx4(gpu(0), gpu(0), -1)
+
+
+@pytest.mark.parametrize("fn, args, short", [
+    (ddp.mx4_quantize_rows, quantize_args, ("rank_in", "rank_residual", "rank_codes", "rank_scales")),
+    (ddp.mx4_dequantize_rows, dequantize_args, ("rank_codes", "rank_scales", "rank_out")),
+    (ddp.allreduce_mx4_rows, reduce_args, ("rank_codes", "rank_scales")),
+    (ddp.allreduce_mx4_coded, coded_args, ("rank_codes", "rank_scales"))])
+def test_fewer_addresses_than_ranks_are_refused(fn, args, short):
+    for name in short:
+        with pytest.raises(ValueError, match="need 2 addresses, got 1"):
+            fn(**args(**{name: [at(20)]}))
 
 
 def test_moments8_sizes():
@@ -323,6 +336,10 @@ def test_tensor_level_refusals(monkeypatch):
         mg.bind_adamw8(w, (gpu(100), gpu(100), gpu(8)))
     with pytest.raises(ValueError):
         ddp.MultiGrad(gpu(99, torch.float32)).bind_adamw8(gpu(99, torch.float32), mom)
+    with pytest.raises(TypeError):
+        mg.bind_adamw(w, None, w)
+    with pytest.raises(TypeError):
+        mg.bind_adamw(w, w, None)
     run = mg.bind_adamw8(w, mom)
     with pytest.raises(ValueError):
         run(1e-3, 1, max_norm=1.0)
