@@ -19,9 +19,9 @@
 // flight at once; float32 results go through LDS to whole lines (without that,
 // 16 bytes of every 32 by an instruction, 125 us; loading codes in the order of
 // whole float32 lines instead, which halves what a load's lanes share of a line,
-// 157).  Two spans a wave, not one, where a span is little to load: 4 ranks
-// coded again 128 us against 138 with every rank written, 47 against 41 with one
-// copy.  Workgroups of 4 waves keep the 128 bytes of scales that 4,096 elements
+// 157).  Two spans a wave, not one, where a span is little to load; coded again into
+// one copy 2, 3 and 4 ranks take 39, 53 and 49 us with one, 31, 38 and 42 with two
+// (4 into every rank 132 and 138).  Workgroups of 4 waves keep the 128 bytes of scales that 4,096 elements
 // have in one or two L2s; one-wave workgroups took 146 us for the first case.
 //
 // One copy runs fastest with the CUs full.  Every rank written as values is
@@ -65,23 +65,25 @@ typedef const __attribute__((address_space(4))) ReduceArgs* KReduce;
 enum { kF32 = 0, kBf16 = 1, kCoded = 2, kCodedLeftF32 = 3, kCodedLeftBf16 = 4 };
 constexpr bool has_f32(int out) { return out == kF32 || out == kCodedLeftF32; }
 
-// s / P, correctly rounded.  For P no power of two by way of the float64
-// quotient, whose rounding to float32 is innocuous, and that from the product
-// with 1 / P and one correction by its remainder, which is exact in a fused
-// multiply-add (Markstein's division; with a float64 division 86.6M elements of
-// 3 ranks coded again took 52 us instead of 46).
+// s / P, correctly rounded.  For P no power of two from the product with 1 / P
+// and one correction by its remainder, which is exact in a fused multiply-add
+// (Markstein's division).  For each of these P that gives the nearest float32 for
+// all 2^23 mantissas of s, and so wherever the quotient is normal.  Below, its last
+// place is 2^-149 and s, a sum of codes, a multiple of 2^-128: the exact quotient
+// is then no tie and at least 1 / 2P of a place from one, the error 2^-24 of that.
+// 86.6M elements of 3 ranks coded again took 46 us with this in float64, 38 now.
 template <int P>
 __device__ __forceinline__ float mean_of(float s) {
     if constexpr ((P & (P - 1)) == 0) {
         return s * (1.0f / static_cast<float>(P));
     } else {
-        constexpr double p = P, r = 1.0 / P;
-        const double x = s, q = x * r;
-        const double m = __builtin_fma(__builtin_fma(-p, q, x), r, q);
+        constexpr float p = P, r = 1.0f / P;
+        const float q = s * r;
+        const float m = __builtin_fmaf(__builtin_fmaf(-p, q, s), r, q);
         // a zero keeps its sign and an infinity is its own quotient, where the
         // remainder would not know
         constexpr int kOrdinary = 0x198;      // normal or subnormal, of either sign
-        return __builtin_amdgcn_classf(s, kOrdinary) ? static_cast<float>(m) : s;
+        return __builtin_amdgcn_classf(s, kOrdinary) ? m : s;
     }
 }
 
