@@ -37,7 +37,9 @@
 // of 256, all loads of both first; a lane has 4 consecutive elements, 16 bytes of
 // the weights, and 8 lanes a block.  Blocks count from the tensor's first element,
 // so tiles do too, wherever that lies in a line.  One span a wave: 223 us, but 252
-// with the count on the GPU, whose powers every wave works out; four 226.  By
+// with the count on the GPU, whose powers every wave works out; four 226.  A short
+// call's waves take one: 1,000 elements 3.9 us instead of 5.0, 1M 5.4 and 5.6, 2M
+// 9.0 and 8.2.  By
 // workgroups per CU 0 (full), 2, 3, 4, 5, 6, 8: 228 261 227 221 227 224 226 us.
 // Addresses and sizes travel in the kernel arguments, as in adamw.hip, 162 tensors
 // a launch (139 with copies of the weights).
@@ -56,12 +58,11 @@ namespace {
 using rr::u32x2;
 using rr::u32x4;
 
-// Workgroups of 4 waves; a wave takes kSpans spans of 256 consecutive elements,
-// a lane 4 of each, 8 lanes a block.
+// Workgroups of 4 waves; a wave takes kSpans spans (one in a short launch) of 256
+// consecutive elements, a lane 4 of each, 8 lanes a block.
 constexpr unsigned kLanes = 256;
 constexpr uint32_t kSpan = 256;
 constexpr int kSpans = 2;
-constexpr uint32_t kTileElems = 4 * kSpans * kSpan;
 constexpr uint32_t kBlockElems = DDP_MX_BLOCK;
 constexpr uint32_t kMaxGrid = 1u << 23;
 // Consecutive tensors of a call, as many as the arguments hold (PARAMS: with
@@ -295,7 +296,7 @@ __device__ __forceinline__ void step_lane(const Streams& x, int64_t at, const La
 }
 
 // GB: bf16 gradients.  PM: the copy, 0 none, 1 float32, 2 bf16.
-template <bool GB, int PM>
+template <bool GB, int PM, int U>
 __global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args<PM != 0>) {
     typedef const __attribute__((address_space(4))) Adam8Args<PM != 0>* KAdam8;
     const KAdam8 a = (KAdam8)(__builtin_amdgcn_kernarg_segment_ptr());
@@ -308,12 +309,12 @@ __global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args<PM != 0>) {
         const int t = piece_of(a, tile);
         const Streams x = {a->g[t], a->w[t], a->m[t], a->v[t], a->s[t], PM != 0 ? a->p[PM != 0 ? t : 0] : nullptr,
                            a->count[t]};
-        const int64_t at = (static_cast<int64_t>(tile - a->first_tile[t]) * 4 + wave) * (kSpans * kSpan);
-        const bool whole = at + kSpans * kSpan <= x.n;
-        Lane l[kSpans];
+        const int64_t at = (static_cast<int64_t>(tile - a->first_tile[t]) * 4 + wave) * (U * kSpan);
+        const bool whole = at + U * kSpan <= x.n;
+        Lane l[U];
         if (whole) {
 #pragma unroll
-            for (int u = 0; u < kSpans; ++u) l[u] = load_lane<GB, true>(x, at + u * kSpan);
+            for (int u = 0; u < U; ++u) l[u] = load_lane<GB, true>(x, at + u * kSpan);
         }
         // The factors (divisions, two powers) and the key while the data is in
         // flight.
@@ -324,24 +325,25 @@ __global__ __launch_bounds__(kLanes) void adamw8_kernel(Adam8Args<PM != 0>) {
         key = mix_word(mix_word(key, a->tensor + t), a->piece);
         if (whole) {
 #pragma unroll
-            for (int u = 0; u < kSpans; ++u) step_lane<GB, PM, true>(x, at + u * kSpan, l[u], f, key);
+            for (int u = 0; u < U; ++u) step_lane<GB, PM, true>(x, at + u * kSpan, l[u], f, key);
         } else {
-            for (int64_t i = at; i < x.n && i < at + kSpans * kSpan; i += kSpan)
+            for (int64_t i = at; i < x.n && i < at + U * kSpan; i += kSpan)
                 step_lane<GB, PM, false>(x, i, load_lane<GB, false>(x, i), f, key);
         }
     }
 }
 
+template <int U>
 const void* kernel_for(const AdamWLaunch& l) {
     const int pm = l.params == nullptr ? 0 : (l.param_bf16 ? 2 : 1);
     if (l.grad_bf16) {
-        return pm == 0 ? reinterpret_cast<const void*>(&adamw8_kernel<true, 0>)
-               : pm == 1 ? reinterpret_cast<const void*>(&adamw8_kernel<true, 1>)
-                         : reinterpret_cast<const void*>(&adamw8_kernel<true, 2>);
+        return pm == 0 ? reinterpret_cast<const void*>(&adamw8_kernel<true, 0, U>)
+               : pm == 1 ? reinterpret_cast<const void*>(&adamw8_kernel<true, 1, U>)
+                         : reinterpret_cast<const void*>(&adamw8_kernel<true, 2, U>);
     }
-    return pm == 0 ? reinterpret_cast<const void*>(&adamw8_kernel<false, 0>)
-           : pm == 1 ? reinterpret_cast<const void*>(&adamw8_kernel<false, 1>)
-                     : reinterpret_cast<const void*>(&adamw8_kernel<false, 2>);
+    return pm == 0 ? reinterpret_cast<const void*>(&adamw8_kernel<false, 0, U>)
+           : pm == 1 ? reinterpret_cast<const void*>(&adamw8_kernel<false, 1, U>)
+                     : reinterpret_cast<const void*>(&adamw8_kernel<false, 2, U>);
 }
 
 // The moments' values.
@@ -460,12 +462,15 @@ int launch_step(const AdamW8Launch& l, const char** msg) {
     Adam8Args<PARAMS> a;
     a.scalars = adamw::scalars_of(b);
     a.seed = mix_word(mix_word(0, static_cast<uint32_t>(l.seed)), static_cast<uint32_t>(l.seed >> 32));
-    const void* fn = kernel_for(b);
+    int64_t all = 0;
+    for (int32_t t = 0; t < b.n_tensors && all <= kMxShort; ++t) all += b.numels[t];
+    const int spans = all <= kMxShort ? 1 : kSpans;
+    const void* fn = spans == 1 ? kernel_for<1>(b) : kernel_for<kSpans>(b);
     int64_t at = 0;
     for (int32_t t = 0; t < b.n_tensors;) {
         a.tensor = static_cast<uint32_t>(t);
         a.piece = static_cast<uint32_t>(at / kMaxPiece);
-        fill_launch(a, b.n_tensors, b.numels, kTileElems, t, at, [&](int k, int32_t i, int64_t from) {
+        fill_launch(a, b.n_tensors, b.numels, 4 * spans * kSpan, t, at, [&](int k, int32_t i, int64_t from) {
             a.g[k] = static_cast<const char*>(b.grads[i]) + from * (b.grad_bf16 ? 2 : 4);
             a.w[k] = reinterpret_cast<char*>(b.w[i] + from);
             a.m[k] = reinterpret_cast<char*>(l.m[i] + from);

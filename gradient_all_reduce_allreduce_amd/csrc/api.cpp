@@ -1874,7 +1874,7 @@ int mx4_reduce(ddp_reduce_op op, int32_t P, const uint8_t* const* codes, const u
         l.scales[r] = scales[r];
     }
     l.n_out = n_out;
-    l.out_type = coded ? 2 : (out_dtype == DDP_BF16 ? 1 : 0);
+    l.out_type = coded ? ddp::kMxCoded : (out_dtype == DDP_BF16 ? ddp::kMxBf16 : ddp::kMxF32);
     for (int r = 0; r < n_out; ++r) {
         l.out[r] = out[r];
         l.out_scales[r] = coded ? out_scales[r] : nullptr;

@@ -16,15 +16,30 @@ constexpr int64_t mx_tiles(int64_t n, int spans) { return (n + 2048 * spans - 1)
 // A grid holds fewer than 2^32 lanes; each workgroup walks on by its size.
 constexpr uint32_t kMaxMxGrid = 1u << 23;
 
+// Elements up to which a launch's waves take one span each, not two: a short one
+// ends no sooner than its longest wave (figures in mx4.hip and adamw8.hip).
+constexpr int64_t kMxShort = 1 << 20;
+
 // Quantisation and reading back: spans per wave, and workgroups per CU (figures
 // in mx4.hip).
 constexpr int kMx4Spans = 2;
 constexpr int mx4_quantize_wg_per_cu(bool left) { return left ? 4 : 6; }
 constexpr int mx4_dequantize_wg_per_cu(bool bf16) { return bf16 ? 5 : 4; }
 
-// The all-reduce (figures in mx4_reduce.hip).  Spans per wave: two where a span
-// moves little, few ranks and no float32.
-constexpr int mx4_reduce_spans(int P, bool f32) { return !f32 && P <= 4 ? 2 : 1; }
+// What the all-reduce writes: values, or codes with the left-over as the last
+// word has it.
+enum Mx4Out { kMxF32 = 0, kMxBf16 = 1, kMxCoded = 2, kMxCodedLeftF32 = 3, kMxCodedLeftBf16 = 4 };
+// The all-reduce (figures in mx4_reduce.hip).  Spans per wave on long rows: more
+// than one where a span moves little, few ranks and neither float32 nor a
+// left-over; `one`: into one copy.
+constexpr int mx4_reduce_spans(int P, int out, bool one) {
+    if (out == kMxBf16) return P <= 4 ? 2 : 1;
+    if (out != kMxCoded) return 1;
+    if (one) return P <= 4 ? 4 : P <= 7 ? 2 : 1;
+    return P <= 2 ? 4 : P <= 3 ? 2 : 1;
+}
+// One while the waves of all spans fit the GPU at once.
+constexpr int64_t kMxOneSpan = 1 << 22;
 // Workgroups per CU, 0 for no limit: fewer the more every rank receives as
 // values; one more of those with float32 and the norm, whose sums they wait for.
 constexpr int mx4_reduce_wg_per_cu(int P, bool f32, bool all_ranks_values, bool norm) {
@@ -61,7 +76,7 @@ struct Mx4Reduce {
     const void* codes[kMaxRanks];
     const void* scales[kMaxRanks];
     int n_out;
-    int out_type;                    // 0 float32, 1 bf16, 2 coded
+    int out_type;                    // Mx4Out without a left-over
     void* out[kMaxRanks];            // coded: the codes
     void* out_scales[kMaxRanks];
     void* left;

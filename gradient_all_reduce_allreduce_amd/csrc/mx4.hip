@@ -21,7 +21,9 @@
 // Layout (mx.h): a wave takes 2 spans of 512 elements, all loads first.  One span
 // leaves too little in flight (bf16 alone 92 us) and starts nearly as many waves
 // as the dispatcher can; with 4 a float32 row's waves hold too much (439 us
-// instead of 398).  A workgroup's 4,096 elements have 128 bytes of scales: one
+// instead of 398).  Short rows are quantised with one: 8 bf16 rows of 1,000
+// elements with bf16 left-overs 3.8 us instead of 5.1, of 262,144 4.3 and 4.4, of
+// 4.2M 39.6 and 37.5 (reading back: no difference).  A workgroup's 4,096 elements have 128 bytes of scales: one
 // line, written by one CU.  By workgroups per CU 0 (full), 2, 3, 4, 5, 6, 8: bf16
 // with left-over 212 236 225 206 207 212 211 us, float32 without 152 180 158 151
 // 145 146 148, bf16 without 86 132 109 95 89 85 85.
@@ -73,10 +75,9 @@ __device__ __forceinline__ void quantize_span(const mx::Raw& g, const mx::Raw& r
     }
 }
 
-template <bool BF16, int LEFT>
+template <bool BF16, int LEFT, int U>
 __global__ __launch_bounds__(kMxLanes) void mx4_quantize_kernel(Mx4Args) {
     constexpr bool W = kWide<BF16, LEFT>;
-    constexpr int U = kMx4Spans;
     const KMx4 a = (KMx4)(__builtin_amdgcn_kernarg_segment_ptr());
     const char* const in = a->values[blockIdx.y];
     char* const left = a->left[blockIdx.y];
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(kMxLanes) void mx4_dequantize_kernel(Mx4Args) {
     }
 }
 
-int launch(const void* fn, const Mx4Launch& l, unsigned lds, const char* what, const char** msg) {
+int launch(const void* fn, const Mx4Launch& l, int spans, unsigned lds, const char* what, const char** msg) {
     Mx4Args a{};
     for (int r = 0; r < l.P; ++r) {
         a.values[r] = static_cast<char*>(const_cast<void*>(l.values[r]));
@@ -153,7 +154,7 @@ int launch(const void* fn, const Mx4Launch& l, unsigned lds, const char* what, c
         a.scales[r] = static_cast<char*>(l.scales[r]);
     }
     a.n = l.n;
-    a.tiles = static_cast<uint32_t>(mx_tiles(l.n, kMx4Spans));
+    a.tiles = static_cast<uint32_t>(mx_tiles(l.n, spans));
     const unsigned grid = std::min(a.tiles, kMaxMxGrid / static_cast<unsigned>(l.P));
     void* args[] = {&a};
     const hipError_t e = hipLaunchKernel(fn, dim3(grid, static_cast<unsigned>(l.P)), dim3(kMxLanes), args, lds,
@@ -166,21 +167,22 @@ int launch(const void* fn, const Mx4Launch& l, unsigned lds, const char* what, c
 }  // namespace
 
 int launch_mx4_quantize(const Mx4Launch& l, const char** msg) {
-    const void* const fns[2][3] = {
-        {reinterpret_cast<const void*>(&mx4_quantize_kernel<false, 0>),
-         reinterpret_cast<const void*>(&mx4_quantize_kernel<false, 1>),
-         reinterpret_cast<const void*>(&mx4_quantize_kernel<false, 2>)},
-        {reinterpret_cast<const void*>(&mx4_quantize_kernel<true, 0>),
-         reinterpret_cast<const void*>(&mx4_quantize_kernel<true, 1>),
-         reinterpret_cast<const void*>(&mx4_quantize_kernel<true, 2>)}};
-    return launch(fns[l.bf16][l.left_type], l, lds_reserve(mx4_quantize_wg_per_cu(l.left_type != 0)),
-                  "hipLaunchKernel(mx4_quantize)", msg);
+#define DDP_KERNELS(BF16, U)                                            \
+    {reinterpret_cast<const void*>(&mx4_quantize_kernel<BF16, 0, U>),   \
+     reinterpret_cast<const void*>(&mx4_quantize_kernel<BF16, 1, U>),   \
+     reinterpret_cast<const void*>(&mx4_quantize_kernel<BF16, 2, U>)}
+    const void* const fns[2][2][3] = {{DDP_KERNELS(false, kMx4Spans), DDP_KERNELS(true, kMx4Spans)},
+                                      {DDP_KERNELS(false, 1), DDP_KERNELS(true, 1)}};
+#undef DDP_KERNELS
+    const bool few = l.n <= kMxShort / l.P;
+    return launch(fns[few][l.bf16][l.left_type], l, few ? 1 : kMx4Spans,
+                  lds_reserve(mx4_quantize_wg_per_cu(l.left_type != 0)), "hipLaunchKernel(mx4_quantize)", msg);
 }
 
 int launch_mx4_dequantize(const Mx4Launch& l, const char** msg) {
     const void* const fn = l.bf16 ? reinterpret_cast<const void*>(&mx4_dequantize_kernel<true>)
                                   : reinterpret_cast<const void*>(&mx4_dequantize_kernel<false>);
-    return launch(fn, l, lds_reserve(mx4_dequantize_wg_per_cu(l.bf16), l.bf16 ? 0 : mx::kExchangeBytes),
+    return launch(fn, l, kMx4Spans, lds_reserve(mx4_dequantize_wg_per_cu(l.bf16), l.bf16 ? 0 : mx::kExchangeBytes),
                   "hipLaunchKernel(mx4_dequantize)", msg);
 }
 

@@ -19,10 +19,17 @@
 // flight at once; float32 results go through LDS to whole lines (without that,
 // 16 bytes of every 32 by an instruction, 125 us; loading codes in the order of
 // whole float32 lines instead, which halves what a load's lanes share of a line,
-// 157).  Two spans a wave, not one, where a span is little to load; coded again into
-// one copy 2, 3 and 4 ranks take 39, 53 and 49 us with one, 31, 38 and 42 with two
-// (4 into every rank 132 and 138).  Workgroups of 4 waves keep the 128 bytes of scales that 4,096 elements
-// have in one or two L2s; one-wave workgroups took 146 us for the first case.
+// 157).  A wave with little to load takes more than one span; us for 86.6M elements
+// coded again by spans 1, 2, 4 --
+//     one copy  P = 2  39 31 26   P = 3  48 38 33   P = 4  47 41 39   P = 6  60 56 57
+//               P = 8  70 73 75
+//     all       P = 2  43 36 31   P = 3  55 50 52   P = 4  67 70 69   P = 6 101 107 106
+//     one copy with a bf16 left-over  P = 2  78 80 80   P = 8  123 129 129
+// (to bf16, one copy: P = 2 59 50 51, P = 4 69 64).  Short rows take one: 2 ranks of
+// 65,536 coded again 2.8 us with one span, 3.5 with four, of 4.2M 4.0 and 4.3, of
+// 8.4M 6.1 and 5.2.  Workgroups of 4 waves keep the 128 bytes of scales that 4,096
+// elements have in one or two L2s; one-wave workgroups took 146 us for the first
+// case.
 //
 // One copy runs fastest with the CUs full.  Every rank written as values is
 // nearly all writes, many streams at once, and wants fewer: us for 86.6M elements by
@@ -60,10 +67,7 @@ struct ReduceArgs {
 };
 typedef const __attribute__((address_space(4))) ReduceArgs* KReduce;
 
-// What a kernel writes: values, or codes with the left-over as the last
-// template argument has it.
-enum { kF32 = 0, kBf16 = 1, kCoded = 2, kCodedLeftF32 = 3, kCodedLeftBf16 = 4 };
-constexpr bool has_f32(int out) { return out == kF32 || out == kCodedLeftF32; }
+constexpr bool has_f32(int out) { return out == kMxF32 || out == kMxCodedLeftF32; }
 
 // s / P, correctly rounded.  For P no power of two from the product with 1 / P
 // and one correction by its remainder, which is exact in a fused multiply-add
@@ -103,11 +107,11 @@ __device__ __forceinline__ void reduce_span(KReduce a, const uint32_t (&c)[P], c
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = mean_of<P>(g[e]);
     }
-    if constexpr (OUT >= kCoded) {
+    if constexpr (OUT >= kMxCoded) {
         float old[8];
-        if constexpr (OUT != kCoded) {
+        if constexpr (OUT != kMxCoded) {
             float (&x)[8] = old;
-            mx::values_of<OUT == kCodedLeftBf16, has_f32(OUT)>(left, x);
+            mx::values_of<OUT == kMxCodedLeftBf16, has_f32(OUT)>(left, x);
             if constexpr (has_f32(OUT)) mx::exchange<false>(*lds, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] += x[e];
@@ -122,7 +126,7 @@ __device__ __forceinline__ void reduce_span(KReduce a, const uint32_t (&c)[P], c
         mx::decode8(q.codes, q.scales, x);
         for (int r = 0; r < a->n_out; ++r)
             mx::store_coded<false, WHOLE>(a->out[r], a->out_scales[r], at, n, q.codes, q.scales);
-        if constexpr (OUT != kCoded) {
+        if constexpr (OUT != kMxCoded) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = g[e] - x[e];
@@ -142,18 +146,17 @@ __device__ __forceinline__ void reduce_span(KReduce a, const uint32_t (&c)[P], c
         for (int e = 0; e < 8; ++e) g[e] = x[e];
     } else {
         if constexpr (has_f32(OUT)) mx::exchange<true>(*lds, g);
-        for (int r = 0; r < a->n_out; ++r) mx::store_values<OUT == kBf16, has_f32(OUT), WHOLE>(a->out[r], at, n, g);
+        for (int r = 0; r < a->n_out; ++r) mx::store_values<OUT == kMxBf16, has_f32(OUT), WHOLE>(a->out[r], at, n, g);
     }
     if (a->partials != nullptr) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (WHOLE || mx::in_row<OUT == kF32>(at, n, e)) sq = rr::square_to(sq, rr::written<OUT == kBf16>(g[e]));
+            if (WHOLE || mx::in_row<OUT == kMxF32>(at, n, e)) sq = rr::square_to(sq, rr::written<OUT == kMxBf16>(g[e]));
     }
 }
 
-template <int P, int OUT>
+template <int P, int OUT, int U>
 __global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
-    constexpr int U = mx4_reduce_spans(P, has_f32(OUT));
     mx::Exchange* const lds = mx::exchange_area<has_f32(OUT)>();
     const KReduce a = (KReduce)(__builtin_amdgcn_kernarg_segment_ptr());
     const int64_t n = a->n;
@@ -171,8 +174,8 @@ __global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
                     c[u][r] = mx::load_codes<false, true>(a->codes[r], at + u * mx::kMxSpan, n);
                     s[u][r] = mx::load_scale<false, true>(a->scales[r], at + u * mx::kMxSpan, n);
                 }
-                if constexpr (OUT > kCoded)
-                    left[u] = mx::load_raw<OUT == kCodedLeftBf16, has_f32(OUT), true>(a->left, at + u * mx::kMxSpan, n);
+                if constexpr (OUT > kMxCoded)
+                    left[u] = mx::load_raw<OUT == kMxCodedLeftBf16, has_f32(OUT), true>(a->left, at + u * mx::kMxSpan, n);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) reduce_span<P, OUT, true>(a, c[u], s[u], left[u], at + u * mx::kMxSpan, n, lds, sq);
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
                     c[0][r] = mx::load_codes<false, false>(a->codes[r], i, n);
                     s[0][r] = mx::load_scale<false, false>(a->scales[r], i, n);
                 }
-                if constexpr (OUT > kCoded) left[0] = mx::load_raw<OUT == kCodedLeftBf16, has_f32(OUT), false>(a->left, i, n);
+                if constexpr (OUT > kMxCoded) left[0] = mx::load_raw<OUT == kMxCodedLeftBf16, has_f32(OUT), false>(a->left, i, n);
                 reduce_span<P, OUT, false>(a, c[0], s[0], left[0], i, n, lds, sq);
             }
         }
@@ -197,12 +200,19 @@ __global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
     }
 }
 
+template <int P, int OUT, int U>
+const void* kernel_of() {
+    if constexpr (U == 1 || U == mx4_reduce_spans(P, OUT, true) || U == mx4_reduce_spans(P, OUT, false))
+        return reinterpret_cast<const void*>(&mx4_reduce_kernel<P, OUT, U>);
+    else
+        return nullptr;
+}
 template <int OUT>
-const void* kernel_for(int P) {
+const void* kernel_for(int P, int spans) {
     switch (P) {
 #define DDP_CASE(p) \
     case p:         \
-        return reinterpret_cast<const void*>(&mx4_reduce_kernel<p, OUT>);
+        return spans == 1 ? kernel_of<p, OUT, 1>() : spans == 2 ? kernel_of<p, OUT, 2>() : kernel_of<p, OUT, 4>();
         DDP_CASE(1) DDP_CASE(2) DDP_CASE(3) DDP_CASE(4)
         DDP_CASE(5) DDP_CASE(6) DDP_CASE(7) DDP_CASE(8)
         DDP_CASE(9) DDP_CASE(10) DDP_CASE(11) DDP_CASE(12)
@@ -233,19 +243,21 @@ int launch_mx4_reduce(const Mx4Reduce& l, int64_t* workgroups, const char** msg)
         a.out[r] = static_cast<char*>(l.out[r]);
         a.out_scales[r] = static_cast<char*>(l.out_scales[r]);
     }
-    const bool coded = l.out_type == kCoded;
+    const bool coded = l.out_type == kMxCoded;
     const int out = l.out_type + (coded ? l.left_type : 0);
     const bool f32 = has_f32(out);
+    const int spans = l.n <= kMxOneSpan ? 1 : mx4_reduce_spans(l.P, out, l.n_out == 1);
     a.left = static_cast<char*>(l.left);
     a.partials = l.partials;
     a.zero = l.zero;
     a.n = l.n;
-    a.tiles = static_cast<uint32_t>(mx_tiles(l.n, mx4_reduce_spans(l.P, f32)));
+    a.tiles = static_cast<uint32_t>(mx_tiles(l.n, spans));
     a.n_out = l.n_out;
     a.mean = l.mean;
-    const void* fn = out == kF32 ? kernel_for<kF32>(l.P) : out == kBf16 ? kernel_for<kBf16>(l.P)
-                     : out == kCoded ? kernel_for<kCoded>(l.P)
-                     : out == kCodedLeftF32 ? kernel_for<kCodedLeftF32>(l.P) : kernel_for<kCodedLeftBf16>(l.P);
+    const void* fn = out == kMxF32 ? kernel_for<kMxF32>(l.P, spans) : out == kMxBf16 ? kernel_for<kMxBf16>(l.P, spans)
+                     : out == kMxCoded ? kernel_for<kMxCoded>(l.P, spans)
+                     : out == kMxCodedLeftF32 ? kernel_for<kMxCodedLeftF32>(l.P, spans)
+                                              : kernel_for<kMxCodedLeftBf16>(l.P, spans);
     const unsigned grid = std::min(a.tiles, kMaxMxGrid);
     *workgroups = grid;
     void* args[] = {&a};

@@ -104,6 +104,14 @@ def test_quantize_anywhere(kind, left_kind, offset):
     check_quantize(2, 1537, kind, left_kind, offset)
 
 
+@pytest.mark.parametrize("left_kind", [None, "f32", "bf16"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("P, n", [(1, 2 ** 20), (1, 2 ** 20 + 1), (2, 2 ** 19 + 513), (3, 350_213)])
+def test_quantize_long(P, n, kind, left_kind):
+    """Up to 2^20 elements in all a wave takes one span, over that two."""
+    check_quantize(P, n, kind, left_kind, offset=1)
+
+
 @pytest.mark.parametrize("P", [1, 2, 5, 16])
 def test_quantize_ranks(P):
     check_quantize(P, 2050, "f32", "f32")
@@ -268,6 +276,52 @@ def test_allreduce_lengths(n, kind):
     check_reduce(3, n, "mean", kind, 1, offset=1)
 
 
+@pytest.mark.parametrize("P", [3, 5, 6, 7, 9, 10, 11, 12, 13, 14, 15])
+@pytest.mark.parametrize("low, high", [(0, 6), (10, 30), (100, 104), (90, 130), (248, 255)])
+def test_mean_is_the_nearest_float32(P, low, high):
+    """Where quotients are subnormal, ordinary and where sums are infinite."""
+    n = 1 << 15
+    rng = np.random.default_rng(P)
+    coded = [(rng.integers(0, 256, n // 2).astype(np.uint8), rng.integers(low, high, n // 32).astype(np.uint8))
+             for _ in range(P)]
+    with np.errstate(all="ignore"):
+        want = mx.mx4_allreduce(np.stack([mx.mx4_decode(c, s, n) for c, s in coded]), "mean")
+    assert_same_bits(ddp.allreduce_mx4(on_gpu(coded, n), "mean")[0].cpu().numpy(), want)
+
+
+LONG = 2 ** 22        # elements from which a wave takes more than one span
+
+
+@pytest.mark.parametrize("P", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("tail", [1, 513, 2049 + 512, 8191])
+def test_long_rows_are_their_parts(P, tail):
+    """A row long enough for waves of several spans, and its parts, which are
+    not: the same codes, values and left-overs, and nothing behind the row."""
+    n = LONG + tail
+    rng = np.random.default_rng(P)
+    coded = [(rng.integers(0, 256, -(-n // 32) * 16).astype(np.uint8),
+              rng.integers(90, 130, -(-n // 32)).astype(np.uint8)) for _ in range(P)]
+    rows = on_gpu(coded, n)
+    parts = [(0, LONG // 2), (LONG // 2, n - LONG // 2)]
+    for copies in {1, P}:
+        out = [guarded_mx(n, 1) for _ in range(copies)]
+        ddp.allreduce_mx4(rows, "mean", out=[x[2] for x in out])
+        values16 = [Guarded(np.zeros(n, f), "bf16", 1) for _ in range(copies)]
+        ddp.allreduce_mx4(rows, "mean", out=[x.view for x in values16])
+        for at, length in parts:
+            mine = [r.narrow(at, length) for r in rows]
+            want = ddp.allreduce_mx4(mine, "mean", out=[ddp.Mx4.empty(length)])[0]
+            want16 = ddp.allreduce_mx4(mine, "mean", out=[torch.empty(length, dtype=torch.bfloat16, device=DEV)])[0]
+            for k in range(copies):
+                got = out[k][2].narrow(at, length)
+                assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales), (copies, at)
+                assert torch.equal(values16[k].view[at:at + length], want16), (copies, at)
+        for x in out:
+            x[0].intact(), x[1].intact()
+        for x in values16:
+            x.intact()
+
+
 def test_allreduce_norm_of_many_workgroups():
     check_reduce(2, 5_000_011, "mean", "f32", 1)
 
@@ -412,6 +466,14 @@ def check_adamw8(numels, kind, params, views, step=3, seed=11, norm=None, max_no
 @pytest.mark.parametrize("sizes", SIZES)
 def test_adamw8(sizes, kind, params, views):
     check_adamw8(SIZES[sizes], kind, params, views, norm=3.0 if views else None, max_norm=1.0 if views else None)
+
+
+@pytest.mark.parametrize("kind, params, views", [("f32", None, True), ("bf16", "bf16", False), ("bf16", "f32", True)])
+@pytest.mark.parametrize("numels", [[700_001, 300_001, 48_574], [700_001, 300_001, 48_575], [1, 1_048_577 + 767, 300, 1057]])
+def test_adamw8_long(numels, kind, params, views):
+    """2^20 elements in all, for which a wave takes one span, and more, for
+    which it takes two."""
+    check_adamw8(numels, kind, params, views, on_gpu=views)
 
 
 @pytest.mark.parametrize("step", [1, 2, 1000, 2 ** 33 + 5])
