@@ -29,20 +29,20 @@
 // everything as it was.
 //
 // Bound by HBM: 16.1 bytes an element with bf16 gradient and copy (32-bit moments:
-// 28) against 64 instructions, 11 of them a wave's own.  86.6M elements, bf16 gradient and copy: 221 us, 6.3
-// TB/s, with the count on the GPU 222; float32 gradient without copy 221, one
-// element off a line 236.  Read back as bf16 82 us, 6.4 TB/s, as float32 130, 6.7.
+// 28) against 64 instructions, 11 of them a wave's own.  86.6M elements, bf16
+// gradient and copy: 221 us, 6.3 TB/s, with the count on the GPU 222; float32
+// gradient without copy 221, one element off a line 236.  Read back as bf16 82 us,
+// 6.4 TB/s, as float32 130, 6.7.
 //
 // Layout: a workgroup of 4 waves takes a tile of 2,048 elements, a wave two spans
 // of 256, all loads of both first; a lane has 4 consecutive elements, 16 bytes of
 // the weights, and 8 lanes a block.  Blocks count from the tensor's first element,
-// so tiles do too, wherever that lies in a line.  One span a wave: 223 us, but 252
-// with the count on the GPU, whose powers every wave works out; four 226.  A short
-// call's waves take one: 1,000 elements 3.9 us instead of 5.0, 1M 5.4 and 5.6, 2M
-// 9.0 and 8.2.  By
-// workgroups per CU 0 (full), 2, 3, 4, 5, 6, 8: 228 261 227 221 227 224 226 us.
-// Addresses and sizes travel in the kernel arguments, as in adamw.hip, 162 tensors
-// a launch (139 with copies of the weights).
+// so tiles do too, wherever that lies in a line.  One span a wave took 267 us, 279
+// with the count on the GPU, when two took 231 and 237; four 226 when two took 221.
+// A short call's waves take one: 1,000 elements 3.9 us instead of 5.0, 1M 5.4 and
+// 5.6, 2M 9.0 and 8.2.  By workgroups per CU 0 (full), 2, 3, 4, 5, 6, 8: 228 261 227
+// 221 227 224 226 us.  Addresses and sizes travel in the kernel arguments, as in
+// adamw.hip, 161 tensors a launch (139 with copies of the weights).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -65,12 +65,13 @@ constexpr uint32_t kSpan = 256;
 constexpr int kSpans = 2;
 constexpr uint32_t kBlockElems = DDP_MX_BLOCK;
 constexpr uint32_t kMaxGrid = 1u << 23;
+constexpr int rows_for(int cap) { return (cap + 15) / 16 * 16; }
 // Consecutive tensors of a call, as many as the arguments hold (PARAMS: with
 // their copies), empty ones among them; or one piece of a tensor that is longer
 // than kMaxPiece.
 template <bool PARAMS>
 struct Adam8Args {
-    static constexpr int kCap = PARAMS ? 139 : 162;
+    static constexpr int kCap = PARAMS ? 139 : 161, kRows = rows_for(kCap);
     const char* g[kCap];
     char* w[kCap];
     char* m[kCap];
@@ -78,7 +79,7 @@ struct Adam8Args {
     char* s[kCap];
     char* p[PARAMS ? kCap : 1];
     uint32_t count[kCap];      // elements
-    uint32_t first_tile[kCap];
+    uint32_t first_tile[kRows];    // behind the last tensor none that a tile can have
     int32_t n;
     uint32_t tiles;
     uint32_t tensor;           // the first one's number in the call
@@ -192,14 +193,20 @@ __device__ __forceinline__ void store_bytes(char* p, int64_t i, int64_t n, uint3
         if (i + e < n) p[i + e] = static_cast<char>(x >> (8 * e));
 }
 
-// The last tensor that starts at or before the tile.
+// The last tensor that starts at or before the tile: counted among every 16th,
+// then among the 16 from there, so that a wave waits for two reads of the
+// arguments.  (A search by halves waits for eight: 400 tensors of 61M elements 202
+// us instead of 200, read back 129 instead of 127; the lanes of a wave looking at
+// all at once wait for vector loads: 204 and 157.)
 template <class A>
 __device__ __forceinline__ int piece_of(A a, uint32_t tile) {
+    if (a->n == 1) return 0;
     int t = 0;
-    for (int h = a->n - 1; t < h;) {
-        const int mid = (t + h + 1) >> 1;
-        if (a->first_tile[mid] <= tile) t = mid; else h = mid - 1;
-    }
+#pragma unroll
+    for (int k = 16; k < a->kRows; k += 16) t += a->first_tile[k] <= tile ? 16 : 0;
+    const auto* const some = &a->first_tile[t];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) t += some[k] <= tile ? 1 : 0;
     return t;
 }
 
@@ -349,14 +356,14 @@ const void* kernel_for(const AdamWLaunch& l) {
 // The moments' values.
 constexpr int read_spans(bool bf16) { return bf16 ? 2 : 1; }
 struct Read8Args {
-    static constexpr int kCap = 164;
+    static constexpr int kCap = 163, kRows = rows_for(kCap);
     const char* m[kCap];
     const char* v[kCap];
     const char* s[kCap];
     char* m_out[kCap];
     char* v_out[kCap];
     uint32_t count[kCap];
-    uint32_t first_tile[kCap];
+    uint32_t first_tile[kRows];    // behind the last tensor none that a tile can have
     int32_t n;
     uint32_t tiles;
 };
@@ -454,6 +461,7 @@ void fill_launch(A& a, int32_t n_tensors, const int64_t* numels, int64_t tile, i
         if (alone) break;
     }
     a.tiles = static_cast<uint32_t>(tiles);
+    std::fill(a.first_tile + a.n, a.first_tile + A::kRows, UINT32_MAX);
 }
 
 template <bool PARAMS>

@@ -817,7 +817,7 @@ def test_same_call_same_bits():
     assert abs(float(share) - 2 * p * (1 - p)) < 0.0046
 
 
-@pytest.mark.parametrize("count", [139, 140, 162, 163, 164, 165, 325])
+@pytest.mark.parametrize("count", [139, 140, 160, 161, 162, 163, 164, 165, 323, 325])
 @pytest.mark.parametrize("params", [None, "bf16"])
 def test_adamw8_at_the_launches_limits(count, params):
     """As many tensors as a launch holds, and one more; every fifth empty, the
