@@ -305,9 +305,11 @@ def test_long_rows_are_their_parts(P, tail):
     parts = [(0, LONG // 2), (LONG // 2, n - LONG // 2)]
     for copies in {1, P}:
         out = [guarded_mx(n, 1) for _ in range(copies)]
-        ddp.allreduce_mx4(rows, "mean", out=[x[2] for x in out])
+        coded_out, norm = ddp.allreduce_mx4_norm(rows, "mean", out=[x[2] for x in out])
         values16 = [Guarded(np.zeros(n, f), "bf16", 1) for _ in range(copies)]
-        ddp.allreduce_mx4(rows, "mean", out=[x.view for x in values16])
+        _, norm16 = ddp.allreduce_mx4_norm(rows, "mean", out=[x.view for x in values16])
+        check_norm(norm, ddp.mx4_dequantize(coded_out[:1])[0].cpu().numpy())
+        check_norm(norm16, values16[0].host())
         for at, length in parts:
             mine = [r.narrow(at, length) for r in rows]
             want = ddp.allreduce_mx4(mine, "mean", out=[ddp.Mx4.empty(length)])[0]
