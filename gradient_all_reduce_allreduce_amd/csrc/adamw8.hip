@@ -24,9 +24,9 @@
 // 0.99, 20% with 0.999, no offset); m, whose steps are larger, by 9% of its own
 // root mean square.
 //
-// A block of m with an infinity or a NaN has s = 255 and is NaN as a whole from
-// the next step on, one of v infinite.  A norm that is not finite leaves
-// everything as it was.
+// A block of m with an infinity or a NaN, of whatever sign and payload, has s = 255
+// and is NaN as a whole from the next step on, one of v infinite.  A norm that is
+// not finite leaves everything as it was.
 //
 // Bound by HBM: 16.1 bytes an element with bf16 gradient and copy (32-bit moments:
 // 28) against 64 instructions, 11 of them a wave's own.  86.6M elements, bf16
@@ -124,8 +124,10 @@ __device__ __forceinline__ uint32_t scale_m(uint32_t top) {
     const uint32_t e = ((((top + 0xfffffu) >> 20) + 1u) >> 3);
     return top < 0x7f800000u ? mx::larger(e, 9u) - 8u : 255u;
 }
+// The same of v; a NaN, which lies above infinity and may have a sign, counts as
+// infinity, so that the sum stays within 32 bits.
 __device__ __forceinline__ uint32_t scale_v(uint32_t top) {
-    const uint32_t e = (top + 0xfffffu) >> 23;
+    const uint32_t e = ((top < 0x7f800000u ? top : 0x7f800000u) + 0xfffffu) >> 23;
     if (top == 0u) return 0u;
     return e < 255u ? mx::larger(e, 32u) : 255u;
 }

@@ -1101,7 +1101,7 @@ int allreduce_mx4_workspace_bytes(int64_t n, int64_t* bytes);
  * identical replicas need the same seed; calls that share a step's tensors
  * among them, and so count each from 0, a seed each.
  * A block of m that meets an infinity or NaN becomes NaN as a whole, one of v
- * that passes float32 infinite.
+ * that meets a NaN or passes float32 infinite.
  *
  *   m, v         HOST arrays [n_tensors] of pointers to one byte per element, at
  *                any address, updated in place

@@ -857,3 +857,30 @@ def test_adamw8_long_tensor_among_short_ones():
         assert np.array_equal(host_of(mom.v[t][at:at + a.size]), v), (t, at)
         for which, want in enumerate(mx.moments_decode(m, v, s)):
             assert_same_bits(host_of(read[which][t][at:at + a.size]), rounded(want, "bf16"), f"{which} of {t} at {at}")
+
+
+@pytest.mark.parametrize("params, norm", [(None, None), ("bf16", 3.0)])
+@pytest.mark.parametrize("kind, nan", [("bf16", 0xFFFF0000), ("bf16", 0xFF810000), ("bf16", 0x7FFF0000),
+                                       ("f32", 0xFFFFFFFF), ("f32", 0xFFF00001), ("f32", 0xFF800001), ("f32", 0x7FFFFFFF)])
+def test_adamw8_of_any_nan(kind, nan, params, norm):
+    """A NaN of either sign and any payload: its block of m NaN, of v infinite,
+    the other blocks as without it; in whole spans and in a tensor's end."""
+    n, places = 2048 + 70, (5, 1000, 2047, 2100)
+    g = values(n, kind, seed=1)
+    g.view(np.uint32)[list(places)] = nan
+    w, (m, v, s) = values(n, "f32", seed=2), moments(n, 3)
+    bits16 = torch.from_numpy((g.view(np.uint32) >> 16).astype(np.uint16).view(np.int16))
+    grad = (bits16.view(torch.bfloat16) if kind == "bf16" else torch.from_numpy(g)).to(DEV)
+    mom = ddp.Moments8(*(torch.from_numpy(x).to(DEV) for x in (m, v, s)))
+    weights = torch.from_numpy(w.copy()).to(DEV)
+    out = torch.zeros(n, dtype=torch_dtype(params), device=DEV) if params else None
+    ddp.adamw8_step(grad, weights, mom, HYPER["lr"], 3, (HYPER["b1"], HYPER["b2"]), HYPER["eps"], HYPER["wd"], params=out,
+                    norm=torch.tensor(norm, device=DEV) if norm else None, max_norm=1.0 if norm else None, seed=6)
+    c = oracle.clip_factor(norm, 1.0) if norm else f(1)
+    bound = mx.weight_bound(g, w, m, v, s, c, *HYPER.values(), 3)
+    hw, hm, hv, hs = mx.adamw8(g, w, m, v, s, c, *HYPER.values(), 3, 6, 0)
+    assert (hs[[2 * (at // 32) + 1 for at in places]] == 255).all() and (hs == 255).sum() == 2 * len(places)
+    assert np.array_equal(host_of(mom.scales[0]), hs)
+    assert np.array_equal(host_of(mom.m[0]), hm) and np.array_equal(host_of(mom.v[0]), hv)
+    assert_weights(weights.cpu().numpy(), hw, bound, "w")
+    assert np.isnan(hw).sum() == len(places)
