@@ -1339,7 +1339,7 @@ struct Span {
 // Nothing the call writes may overlap anything else.  Sorted by start, a
 // buffer must begin past the end of every written one before it, and a
 // written one past the end of every one before it.
-int check_sorted(const Span* first, const Span* last, uintptr_t* end, bool* writes) {
+int check_sorted(const Span* first, const Span* last) {
     uintptr_t any = 0, written = 0;
     for (const Span* s = first; s != last; ++s) {
         if (s->lo < written || (s->written && s->lo < any))
@@ -1347,16 +1347,23 @@ int check_sorted(const Span* first, const Span* last, uintptr_t* end, bool* writ
         any = std::max(any, s->hi);
         if (s->written) written = std::max(written, s->hi);
     }
-    *end = any;
-    *writes = written != 0;
     return DDP_OK;
 }
 
-// Lists come one after another, and each mostly lies in order in memory of its
-// own: such runs are checked as they are, and against each other as wholes,
-// which for 5 lists of 1,200 tensors saves 200 us of sorting.
+// A call's lists come one after another, and each mostly lies in order in memory
+// of its own, wherever that is.  Such runs are checked as they are once their
+// extents are found to be apart: 6 lists of 400 (1,200) tensors take 5 (16) us in
+// every order of the lists; sorted they take 30 (115).  A run ends with its list
+// (`what`): one that went on into the next list higher up would reach over lists
+// in between.  Lists that reach into each other, or a list in no order, are
+// sorted.
 int check_written(std::vector<Span>& spans) {
+    const auto by_start = [](const Span& x, const Span& y) { return x.lo < y.lo; };
+    Span* const first = spans.data();
+    Span* const last = first + spans.size();
+    if (std::is_sorted(first, last, by_start)) return check_sorted(first, last);
     struct Run {
+        const Span* end;
         uintptr_t lo, hi;
         bool writes;
     };
@@ -1364,26 +1371,26 @@ int check_written(std::vector<Span>& spans) {
     Run runs[kMaxRuns];
     int count = 0;
     bool apart = true;
-    for (size_t at = 0; at < spans.size() && apart;) {
-        size_t end = at + 1;
-        while (end < spans.size() && spans[end].lo >= spans[end - 1].lo) ++end;
-        if (count == kMaxRuns) {
-            apart = false;
-            break;
+    const Span* at = first;
+    while (apart && at != last && count < kMaxRuns) {
+        Run r{at + 1, at->lo, at->hi, at->written};
+        for (; r.end != last && r.end->what == at->what && r.end->lo >= r.end[-1].lo; ++r.end) {
+            r.hi = std::max(r.hi, r.end->hi);
+            r.writes |= r.end->written;
         }
-        Run& r = runs[count];
-        r.lo = spans[at].lo;
-        if (const int s = check_sorted(&spans[at], &spans[0] + end, &r.hi, &r.writes)) return s;
         for (int k = 0; k < count; ++k)
             if ((r.writes || runs[k].writes) && r.lo < runs[k].hi && runs[k].lo < r.hi) apart = false;
-        ++count;
-        at = end;
+        at = r.end;
+        runs[count++] = r;
     }
-    if (apart) return DDP_OK;
-    std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
-    uintptr_t hi;
-    bool writes;
-    return check_sorted(spans.data(), spans.data() + spans.size(), &hi, &writes);
+    if (!apart || at != last) {
+        std::sort(first, last, by_start);
+        return check_sorted(first, last);
+    }
+    at = first;
+    for (int k = 0; k < count; at = runs[k++].end)
+        if (const int s = check_sorted(at, runs[k].end)) return s;
+    return DDP_OK;
 }
 
 // Runs a call's body; host memory that runs out is a status, not an
