@@ -171,12 +171,12 @@ def mx4_dequantize(coded, out=None, dtype=None):
 
 def allreduce_mx4(coded, op="sum", out=None, out_dtype=None, residual=None):
     """All-reduce P coded rank gradients: their values added in float32 in rank
-    order, divided by P for "mean".  ``out``: P tensors or one (a single copy),
-    float32 or bfloat16; or P ``Mx4`` or one, and the result is coded again (rows
-    may be the inputs), with ``residual`` the owner's error from step to step
-    (one float32 or bfloat16 tensor) if given.  Default: P new tensors of
-    ``out_dtype`` (default float32).  Enqueued on the current stream; returns the
-    outputs."""
+    order, divided by P for "mean".  ``out``: P tensors or one (a single copy,
+    in a list or by itself), float32 or bfloat16; or P ``Mx4`` or one, and the
+    result is coded again (rows may be the inputs), with ``residual`` the owner's
+    error from step to step (one float32 or bfloat16 tensor) if given.  Default: P
+    new tensors of ``out_dtype`` (default float32).  Enqueued on the current
+    stream; returns the list of outputs."""
     return _allreduce(coded, op, out, out_dtype, residual, False)[0]
 
 
@@ -195,7 +195,12 @@ def _allreduce(coded, op, out, out_dtype, residual, with_norm):
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             return _allreduce(coded, op, out, out_dtype, residual, with_norm)
-    out = list(out) if out is not None else _new_rows(P, n, out_dtype or torch.float32, device)
+    if out is None:
+        out = _new_rows(P, n, out_dtype or torch.float32, device)
+    elif isinstance(out, Mx4) or (isinstance(out, torch.Tensor) and out.dim() < 2):
+        out = [out]
+    else:
+        out = list(out)
     again = any(isinstance(o, Mx4) for o in out)
     if again:
         out, out_codes, out_scales = _coded_rows(out, "allreduce_mx4 out")

@@ -527,3 +527,28 @@ def test_whole_lists_need_no_sorting_in_any_order():
     orders = [random.Random(k).sample(names, 6) for k in range(8)] + [names[::-1], ["params", "grads", "m", "v", "scales", "w"]]
     for order in orders:
         assert host_time(order) < 2.5 * in_order, order
+
+
+def test_one_output_without_a_list(lib):
+    """A single copy may be given as the tensor or the Mx4 itself; a tensor of
+    rows is still a list of them."""
+    class OnDevice(Gpu):
+        def get_device(self):
+            return None                                 # as its device's index
+
+    def f32(*shape):
+        return torch.Tensor._make_subclass(OnDevice, torch.zeros(*shape))
+
+    rows = [ddp.Mx4(gpu(64), gpu(4), 100) for _ in range(3)]
+    grad, coded = f32(100), ddp.Mx4(gpu(64), gpu(4), 100)
+    assert ddp.allreduce_mx4(rows, "mean", out=grad)[0] is grad
+    assert ddp.allreduce_mx4(rows, "mean", out=[grad])[0] is grad
+    assert ddp.allreduce_mx4(rows, "mean", out=coded, residual=f32(100))[0] is coded
+    (name, args), again, (coded_name, coded_args) = lib.calls
+    assert name == "allreduce_mx4" and (args[5], args[6][0]) == (1, grad.data_ptr())
+    assert again[1][5] == 1 and again[1][6][0] == grad.data_ptr()
+    assert coded_name == "allreduce_mx4_coded" and (coded_args[5], coded_args[6][0]) == (1, coded.codes_at)
+    assert len(ddp.allreduce_mx4(rows, "sum", out=f32(3, 100))) == 3 and lib.calls[-1][1][5] == 3
+    for wrong in (f32(99), f32(101)):
+        with pytest.raises(ValueError, match="out must match"):
+            ddp.allreduce_mx4(rows, out=wrong)
