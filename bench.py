@@ -777,7 +777,7 @@ def _w_mx4_quantize(ctx):
     left = [[x[:plan.total] for x in plan.alloc_arena(8, torch.bfloat16).zero_()] for _ in range(2)]
     return Work("resnet50 p8 f32 gradients to 4 bits with bf16 residuals, every rank's flat buffer",
                 lambda i: ddp.mx4_quantize(rows[i % 2][0], residual=left[i % 2], out=coded[i % 2]),
-                8 * plan.total * (4 + 2 + 2 + 17 / 32), "mx4_quantize_kernel<false, 2>", 1)
+                8 * plan.total * (4 + 2 + 2 + 17 / 32), "mx4_quantize_kernel<false, 2, 2>", 1)
 
 
 def _vit_mx4(ctx):
@@ -802,7 +802,7 @@ def _w_mx4_reduce(ctx):
     outs = [torch.empty(plan.total, device=_dev()) for _ in range(2)]
     return Work("vitb16 p8 4-bit gradients: mean into one float32 copy with its norm",
                 lambda i: ddp.allreduce_mx4_norm(coded[i % 2], "mean", out=[outs[i % 2]]),
-                plan.total * (8 * 17 / 32 + 4), "mx4_reduce_kernel<8, 0>", 2)
+                plan.total * (8 * 17 / 32 + 4), "mx4_reduce_kernel<8, 0, 1>", 2)
 
 
 def _vit_adamw8(ctx):
@@ -827,7 +827,7 @@ def _w_adamw8(ctx):
     norm = torch.full((), 9.3, device=_dev())
     return Work("vitb16 f32 gradient (flat), clipped AdamW step on fp32 w and 8-bit moments with a bf16 copy",
                 lambda i: step(1e-3, i + 1, norm=norm, max_norm=1.0), plan.total * (4 + 8 + 4 + 1 / 8 + 2),
-                "adamw8_kernel<false, 2>", 1)
+                "adamw8_kernel<false, 2, 2>", 1)
 
 
 @work("train-step-mx4-vitb16", "vit")

@@ -71,3 +71,20 @@ def test_source_hash_ignores_comments_but_not_code(tmp_path, monkeypatch):
     assert bench.kernel_source_hash() == h0
     f.write_text(f.read_text() + "static const int kUnused = 1;\n")
     assert bench.kernel_source_hash() != h0
+
+
+def test_the_suites_kernels_exist():
+    """Every kernel that a workload names is one that the library holds, with
+    all its template arguments: a trace filtered by the name finds it."""
+    import re
+    import shutil
+
+    import pytest
+    lib = os.path.join(ROOT, "gradient_all_reduce_allreduce_amd", "libddp_allreduce.so")
+    if shutil.which("nm") is None or not os.path.exists(lib):
+        pytest.skip("needs nm and the built library")
+    symbols = subprocess.run(["nm", "-C", lib], capture_output=True, text=True, check=True).stdout
+    held = set(re.findall(r"__device_stub__(\w+(?:<[^>]*>)?)\(", symbols))
+    with open(os.path.join(ROOT, "bench.py")) as f:
+        named = set(re.findall(r'"(\w+_kernel(?:<[^"]*>)?)"', f.read()))
+    assert len(named) > 15 and not named - held, sorted(named - held)
