@@ -58,10 +58,12 @@ __device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(s
 // codes, 16 of bf16, a quad of lanes a block.  Of float32 a lane would reach
 // over 32 bytes, and an instruction would write every line by halves (which
 // reach memory as halves when the second one comes late: decoding 8 rows to
-// float32 took 1.6 times as long).  So with float32 among a kernel's rows (WIDE)
-// lane l holds the elements 4l .. 4l + 3 and 256 + 4l .. 256 + 4l + 3 of the
-// span, 16 bytes of consecutive kilobytes, 8 lanes a block; a pair of lanes
-// shares two dwords of codes, which it exchanges in registers.
+// float32 took 1.6 times as long).  So float32 goes WIDE: lane l holds the
+// elements 4l .. 4l + 3 and 256 + 4l .. 256 + 4l + 3 of the span, 16 bytes of
+// consecutive kilobytes, 8 lanes a block.  Quantisation and the moments' reading
+// are wide as wholes where float32 is among their rows, and a pair of lanes shares
+// two dwords of codes, or two blocks' scales, which it exchanges in registers;
+// kernels that load codes load them naturally and exchange the values through LDS.
 constexpr int kMxWaves = 4;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
@@ -73,9 +75,9 @@ __device__ __forceinline__ int64_t first4(int64_t at) {
 }
 constexpr int second_after(bool wide) { return wide ? 256 : 4; }
 
-// A dword of codes and a scale byte of the span, as this lane loads or stores
-// them; WIDE: even lanes those of the first four elements of both lanes of a
-// pair, odd lanes those of the second.
+// Where this lane's dword of codes and its scale byte lie in the span; WIDE (codes
+// are only stored so): even lanes have those of the first four elements of both
+// lanes of a pair, odd lanes those of the second.
 template <bool WIDE>
 __device__ __forceinline__ int code_place() {      // in bytes
     const int l = lane_id();
@@ -87,15 +89,11 @@ __device__ __forceinline__ int scale_place() {
     return WIDE ? (l >> 3) + (l & 1) * 8 : l >> 2;
 }
 
-// Between that dword and the codes of this lane's own 8 elements.
+// From the codes of this lane's own 8 elements to that dword.
 __device__ __forceinline__ uint32_t halves() { return (lane_id() & 1) ? 0x07060302u : 0x05040100u; }
 template <bool WIDE>
-__device__ __forceinline__ uint32_t own_codes(uint32_t c) {
-    return WIDE ? __builtin_amdgcn_perm(lane<0xF5>(c), lane<0xA0>(c), halves()) : c;
-}
-template <bool WIDE>
 __device__ __forceinline__ uint32_t shared_codes(uint32_t c) {
-    return own_codes<WIDE>(c);      // its own inverse
+    return WIDE ? __builtin_amdgcn_perm(lane<0xF5>(c), lane<0xA0>(c), halves()) : c;
 }
 
 // The scales of a lane's first and second four elements.
@@ -290,13 +288,14 @@ template <bool WIDE, bool WHOLE>
 __device__ __forceinline__ bool block_in_row(int64_t at, int64_t n) {
     return WHOLE || at + scale_place<WIDE>() * kMxBlock < n;
 }
-template <bool WIDE, bool WHOLE>
+// (Loaded naturally by every kernel.)
+template <bool WHOLE>
 __device__ __forceinline__ uint32_t load_codes(const char* p, int64_t at, int64_t n) {
-    return block_in_row<WIDE, WHOLE>(at, n) ? __builtin_nontemporal_load((GlobalCodes)(p + at / 2 + code_place<WIDE>())) : 0u;
+    return block_in_row<false, WHOLE>(at, n) ? __builtin_nontemporal_load((GlobalCodes)(p + at / 2 + code_place<false>())) : 0u;
 }
-template <bool WIDE, bool WHOLE>
+template <bool WHOLE>
 __device__ __forceinline__ uint32_t load_scale(const char* p, int64_t at, int64_t n) {
-    return block_in_row<WIDE, WHOLE>(at, n) ? *(GlobalBytes)(p + at / kMxBlock + scale_place<WIDE>()) : 0u;
+    return block_in_row<false, WHOLE>(at, n) ? *(GlobalBytes)(p + at / kMxBlock + scale_place<false>()) : 0u;
 }
 // `c`: shared_codes of the lane's own.
 template <bool WIDE, bool WHOLE>

@@ -132,15 +132,15 @@ __global__ __launch_bounds__(kMxLanes) void mx4_dequantize_kernel(Mx4Args) {
         if (at + U * mx::kMxSpan <= n) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                c[u] = mx::load_codes<false, true>(codes, at + u * mx::kMxSpan, n);
-                s[u] = mx::load_scale<false, true>(scales, at + u * mx::kMxSpan, n);
+                c[u] = mx::load_codes<true>(codes, at + u * mx::kMxSpan, n);
+                s[u] = mx::load_scale<true>(scales, at + u * mx::kMxSpan, n);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) dequantize_span<BF16, true>(c[u], s[u], out, at + u * mx::kMxSpan, n, lds);
         } else {
             for (int64_t i = at; i < n; i += mx::kMxSpan)
-                dequantize_span<BF16, false>(mx::load_codes<false, false>(codes, i, n),
-                                             mx::load_scale<false, false>(scales, i, n), out, i, n, lds);
+                dequantize_span<BF16, false>(mx::load_codes<false>(codes, i, n),
+                                             mx::load_scale<false>(scales, i, n), out, i, n, lds);
         }
     }
 }

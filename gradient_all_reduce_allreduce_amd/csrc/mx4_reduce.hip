@@ -171,8 +171,8 @@ __global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int r = 0; r < P; ++r) {
-                    c[u][r] = mx::load_codes<false, true>(a->codes[r], at + u * mx::kMxSpan, n);
-                    s[u][r] = mx::load_scale<false, true>(a->scales[r], at + u * mx::kMxSpan, n);
+                    c[u][r] = mx::load_codes<true>(a->codes[r], at + u * mx::kMxSpan, n);
+                    s[u][r] = mx::load_scale<true>(a->scales[r], at + u * mx::kMxSpan, n);
                 }
                 if constexpr (OUT > kMxCoded)
                     left[u] = mx::load_raw<OUT == kMxCodedLeftBf16, has_f32(OUT), true>(a->left, at + u * mx::kMxSpan, n);
@@ -183,8 +183,8 @@ __global__ __launch_bounds__(kMxLanes) void mx4_reduce_kernel(ReduceArgs) {
             for (int64_t i = at; i < n; i += mx::kMxSpan) {
 #pragma unroll
                 for (int r = 0; r < P; ++r) {
-                    c[0][r] = mx::load_codes<false, false>(a->codes[r], i, n);
-                    s[0][r] = mx::load_scale<false, false>(a->scales[r], i, n);
+                    c[0][r] = mx::load_codes<false>(a->codes[r], i, n);
+                    s[0][r] = mx::load_scale<false>(a->scales[r], i, n);
                 }
                 if constexpr (OUT > kMxCoded) left[0] = mx::load_raw<OUT == kMxCodedLeftBf16, has_f32(OUT), false>(a->left, i, n);
                 reduce_span<P, OUT, false>(a, c[0], s[0], left[0], i, n, lds, sq);
