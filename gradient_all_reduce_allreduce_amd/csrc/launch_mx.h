@@ -41,10 +41,11 @@ constexpr int mx4_reduce_spans(int P, int out, bool one) {
 // One while the waves of all spans fit the GPU at once.
 constexpr int64_t kMxOneSpan = 1 << 22;
 // Workgroups per CU, 0 for no limit: fewer the more every rank receives as
-// values; one more of those with float32 and the norm, whose sums they wait for.
+// values, but not where the waves wait for the norm's sums: up to 6 ranks one more
+// for float32 (from 7 on one is best with the norm too), for bf16 no fewer than 3.
 constexpr int mx4_reduce_wg_per_cu(int P, bool f32, bool all_ranks_values, bool norm) {
     if (!all_ranks_values) return 0;
-    if (!f32) return P <= 6 ? 5 : P <= 12 ? 3 : 1;
+    if (!f32) return P <= 6 ? 5 : P <= 12 || norm ? 3 : 1;
     if (P > 6) return 1;
     return (P <= 2 ? 5 : P <= 3 ? 4 : 2) + (norm ? 1 : 0);
 }

@@ -34,13 +34,44 @@
 // One copy runs fastest with the CUs full.  Every rank written as values is
 // nearly all writes, many streams at once, and wants fewer: us for 86.6M elements by
 // workgroups per CU 0 (full), 1, 2, 3, 4, 5, 6 --
-//     float32  P = 2   151  230  164  149  131  125  147
-//              P = 4   314  331  273  274  304  306  308
-//              P = 8   643  537  602  621  624  632  644
-//     bf16     P = 2    74  130   99   81   73   72   74
-//              P = 8   326  403  328  306  311  331  331
-//     with norm, float32  P = 2  154  285  217  174  155  138  132
-//                         P = 4  318  336  357  274  297  310  312
+//     float32  P = 2    151  230  164  149  131  125  147
+//              P = 3    229  278  237  213  201  226
+//              P = 4    314  331  273  274  304  306  308
+//              P = 6    477  482  448  459  464  468
+//              P = 7    560  515  523  537  543  543
+//              P = 8    643  537  602  621  624  632  644
+//              P = 16  1305 1209 1234 1273
+//     bf16     P = 2     74  130   99   81   73   72   74
+//              P = 6    250  303  280  232  226  225
+//              P = 7    283  351  326  265  261  278
+//              P = 8    326  403  328  306  311  331  331
+//              P = 12   490  503  501  475  504  489
+//              P = 13   536  517  518  530  553  534
+//              P = 16   669  629  665  644  679  656
+// and with the norm --
+//     float32  P = 2    154  285  217  174  155  138  132
+//              P = 3    234  294  267  255  227  200
+//              P = 4    318  336  357  274  297  310  312
+//              P = 6    484  517  541  460  469  470
+//              P = 7    561  515  595  544  553  548
+//              P = 8    645  557  561  624  633  632
+//              P = 10   813  717  706  788  795  799
+//              P = 16  1301 1213 1272 1265 1276 1286
+//     bf16     P = 2     78  191  117   98   84   78
+//              P = 6    251  423  300  241  231  229
+//              P = 8    322  458  363  302  303  311
+//              P = 12   495  568  533  480  490  509
+//              P = 13   541  584  598  521  552  549
+//              P = 16   671  673  685  640  672  653
+// The rules in launch_mx.h are within 2% of the best of each row.  Coded again,
+// every rank is written two streams of 16 and 1 bytes a block; full CUs are within
+// 1% of the best up to 4 ranks, and 2 to 5% above it from 7 on --
+//              P = 4     65            120   96   80   71
+//              P = 7    114  328  211  159  130  114  112
+//              P = 8    133  337  217  164  134  128  127
+//              P = 12   201  446  262  216  196  195  196
+//              P = 16   275  528  303  271  262  265  269
+// (floors at 6.7 TB/s 55, 96, 110, 165, 220).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
