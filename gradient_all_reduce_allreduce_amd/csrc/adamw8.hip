@@ -157,10 +157,12 @@ __device__ __forceinline__ uint32_t top_bytes(const uint32_t (&x)[4]) {
 
 // The weights' step, the root and the quotient by the hardware's instructions,
 // within 1 ulp each: beside moments of 3 bits of mantissa a correctly rounded one
-// says nothing more.  (With those, and codes made by conversions, comparisons and
-// selections, an element took 93 instructions instead of 53, and the step was bound
-// by them, 229 us.)  A second moment below 2^-126, which these instructions take for zero,
-// counts as that.
+// says nothing more (the largest error of float32 weights grows by some 2%).  Both
+// rounded correctly cost what bf16 gradients leave of the instructions' time: 86.6M
+// elements with a bf16 copy 231 us instead of 223, with the count on the GPU too 238
+// instead of 221, without a copy 208 instead of 193; float32 gradients 219 and 218.
+// A second moment below 2^-126, which these instructions take for zero, counts as
+// that.
 __device__ __forceinline__ float step_weight(float w, float m, float v, const adamw::Factors& f) {
 #pragma clang fp contract(off)
     const float least = __uint_as_float(mx::larger(__float_as_uint(v), 1u << 23));

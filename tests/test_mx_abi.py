@@ -505,7 +505,7 @@ def test_adamw8_overlaps_in_any_order_of_lists(which):
 def test_whole_lists_need_no_sorting_in_any_order():
     """What the overlap check takes where every list lies whole and in order,
     whatever the lists' order among each other, is near what it takes where one
-    lies behind the other (sorting took 4 to 7 times as long).  The last copy
+    lies behind the other (sorted they took up to 5 times as long).  The last copy
     overlaps the one before it, so that no call gets past the check."""
     import random
     import time
