@@ -197,8 +197,8 @@ def _allreduce(coded, op, out, out_dtype, residual, with_norm):
             return _allreduce(coded, op, out, out_dtype, residual, with_norm)
     if out is None:
         out = _new_rows(P, n, out_dtype or torch.float32, device)
-    elif isinstance(out, Mx4) or (isinstance(out, torch.Tensor) and out.dim() < 2):
-        out = [out]
+    elif isinstance(out, Mx4) or (isinstance(out, torch.Tensor) and out.dim() < 2 and not n == 1 < out.numel()):
+        out = [out]     # (a longer tensor where n is 1 holds rows of one element)
     else:
         out = list(out)
     again = any(isinstance(o, Mx4) for o in out)

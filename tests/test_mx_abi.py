@@ -552,3 +552,5 @@ def test_one_output_without_a_list(lib):
     for wrong in (f32(99), f32(101)):
         with pytest.raises(ValueError, match="out must match"):
             ddp.allreduce_mx4(rows, out=wrong)
+    ones = [ddp.Mx4(gpu(16), gpu(1), 1) for _ in range(3)]
+    assert len(ddp.allreduce_mx4(ones, out=f32(3))) == 3 and len(ddp.allreduce_mx4(ones, out=f32(1))) == 1
